@@ -376,6 +376,106 @@ moe_status_t moe_route_noalloc(int64_t T, int32_t E, int32_t k, const float* log
                                int32_t* counts, int32_t* offsets, int32_t* perm_src, int32_t* dest,
                                moe_stream_t stream);
 
+/* ---------------------------------------------------------------- training operators around the layer
+ * Layer norm in front of the layer, and the loss head behind it.  These entry
+ * points need no plan: workspace and outputs are the caller's, nothing is
+ * allocated or synchronised, and every sum has one fixed order (bitwise
+ * repeatable).  The pages have no counterpart; the formulas are stated here. */
+
+/* Layer norm over the last dimension of a row-major [rows, d] matrix:
+ *   mean = sum x / d,  rstd = 1 / sqrt(sum (x - mean)^2 / d + eps),
+ *   y = (x - mean) rstd w + b                    (fp32, one rounding to y's type)
+ *   x, y  [rows, d] bf16, or fp32 with x_f32;  w, b [d] bf16, or fp32 with
+ *         w_f32 (b may be NULL);  mean, rstd [rows] fp32, written.
+ * rows >= 0 (0 is a no-op), 1 <= d <= 2^20, eps >= 0.  MOE_ERR_INVALID_ARG for
+ * a null pointer, a tensor that is not 16-byte aligned, or a size or eps out
+ * of range; nothing is enqueued then. */
+moe_status_t moe_layer_norm_forward(const void* x, const void* w, const void* b, int64_t rows, int64_t d,
+                                    int32_t x_f32, int32_t w_f32, float eps, void* y, float* mean, float* rstd,
+                                    moe_stream_t stream);
+
+/* Bytes of workspace moe_layer_norm_backward needs. */
+moe_status_t moe_layer_norm_workspace_bytes(int64_t rows, int64_t d, size_t* bytes);
+
+/* Its backward from the saved statistics.  With n = (x - mean) rstd, g = dy w:
+ *   dx = rstd (g - sum g / d - n sum(g n) / d)   [rows, d], x's type
+ *   dw = sum over rows of dy n,  db = sum over rows of dy   [d], w's type
+ * dy has x's type.  dx, dw or db may be NULL to skip it.  workspace: 256-byte
+ * aligned, moe_layer_norm_workspace_bytes(rows, d) bytes.  With rows = 0, dw
+ * and db are zeroed.  Errors as for the forward. */
+moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* w, const float* mean,
+                                     const float* rstd, int64_t rows, int64_t d, int32_t x_f32, int32_t w_f32,
+                                     void* dx, void* dw, void* db, void* workspace, size_t workspace_bytes,
+                                     moe_stream_t stream);
+
+/* The loss head: logits z = X W^T of T tokens over a vocabulary of V entries,
+ * which are computed in tiles and never stored. */
+typedef struct {
+  int64_t T;               /* tokens, 0 <= T <= 2^20 */
+  int64_t V;               /* vocabulary, 1 <= V <= 2^24 */
+  int32_t d;               /* width; a multiple of 8, at most 2^16 */
+  int32_t K;               /* distillation: teacher entries per token, 1 <= K <= 1024 */
+  float temperature;       /* distillation: > 0 */
+  int32_t ids_int64;       /* labels / ids are int64 (otherwise int32) */
+  int32_t teacher_bf16;    /* distillation: teacher logits are bf16 (otherwise fp32) */
+  int64_t piece;           /* backward: vocabulary columns handled at a time; 0 = default */
+  int64_t wait_timeout_ns; /* bound on every device-side wait; 0 = 2e9 (2 s) */
+  uint32_t debug_flags;    /* MOE_DEBUG_STALL_TEST: the GEMMs' producers issue no loads */
+} moe_head_config_t;
+
+/* Bytes of workspace one call needs (256-byte aligned; for the device that
+ * is current). */
+moe_status_t moe_head_workspace_bytes(const moe_head_config_t* cfg, int32_t distill, int32_t backward,
+                                      size_t* bytes);
+
+/* Softmax cross entropy of each token's label:
+ *   lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t[label_t]
+ * A label outside [0, V) marks a token without a loss: loss_t = lse_t = 0,
+ * and whatever its row of X holds takes part in nothing.
+ *   X [T, d] bf16, W [V, d] bf16, labels [T];  loss, lse [T] fp32, written.
+ * Logits are bf16 products in fp32 sums (exact to about 1e-6 of a logit).
+ * status: a device int32 that receives MOE_ERR_TIMEOUT when a device-side
+ * wait expires (outputs are then not valid), or NULL; it is never cleared.
+ * Errors, synchronous with nothing enqueued: MOE_ERR_INVALID_ARG for a null
+ * or misaligned pointer (tensors 16 bytes, row vectors and ids their own
+ * size, workspace 256), a size out of range or a workspace too small;
+ * MOE_ERR_UNSUPPORTED for d not a multiple of 8 or another GPU. */
+moe_status_t moe_cross_entropy_forward(const moe_head_config_t* cfg, const void* X, const void* W,
+                                       const void* labels, float* loss, float* lse, void* workspace,
+                                       size_t workspace_bytes, int32_t* status, moe_stream_t stream);
+
+/* Its gradient for upstream dloss [T] fp32, from the saved lse:
+ *   D_tv = dloss_t (exp(z_tv - lse_t) - [v = label_t]),  dX = D W,  dW = D^T X
+ * dX [T, d] bf16 and dW [V, d] bf16 are overwritten; either may be NULL to
+ * skip it.  Tokens without a loss, or with dloss_t = 0, get a zero row of dX
+ * and add nothing to dW.  D is formed piece by piece of the vocabulary and
+ * rounded to bf16 for the tensor cores, after a factor common to every
+ * dloss_t was taken out (it multiplies the fp32 sums); the sums are rounded
+ * once.  With T = 0, dW is zeroed. */
+moe_status_t moe_cross_entropy_backward(const moe_head_config_t* cfg, const float* dloss, const void* X,
+                                        const void* W, const void* labels, const float* lse, void* dX, void* dW,
+                                        void* workspace, size_t workspace_bytes, int32_t* status,
+                                        moe_stream_t stream);
+
+/* Distillation from a teacher's K largest logits (or any K) per token.  With
+ * temperature s, p_t = softmax over the token's entries in use of
+ * teacher_tk / s, and q_t = softmax over the whole vocabulary of z_t / s:
+ *   lse_t = log sum_v exp(z_tv / s),
+ *   loss_t = s^2 sum_k p_tk (log p_tk - log q_t[ids_tk])
+ * (s^2 keeps the gradient's size as the temperature changes).  An entry whose
+ * id lies outside [0, V), or whose logit is -inf, is not in use; equal ids
+ * add up.  A token without entries has no loss (as above).
+ *   teacher [T, K] fp32 or bf16, ids [T, K]; the rest as above. */
+moe_status_t moe_distill_forward(const moe_head_config_t* cfg, const void* X, const void* W, const void* teacher,
+                                 const void* ids, float* loss, float* lse, void* workspace,
+                                 size_t workspace_bytes, int32_t* status, moe_stream_t stream);
+
+/* Its gradient with respect to X and W (the teacher gets none):
+ *   D_tv = dloss_t s (q_tv - sum_k p_tk [ids_tk = v]),  dX = D W,  dW = D^T X */
+moe_status_t moe_distill_backward(const moe_head_config_t* cfg, const float* dloss, const void* X, const void* W,
+                                  const void* teacher, const void* ids, const float* lse, void* dX, void* dW,
+                                  void* workspace, size_t workspace_bytes, int32_t* status, moe_stream_t stream);
+
 /* Static description of a status code. */
 const char* moe_status_string(moe_status_t s);
 

@@ -1,0 +1,388 @@
+// head.cu -- the C ABI of the loss head (include/moe.h): argument checks,
+// workspace layout, tensor maps and the kernel sequence of cross entropy and
+// distillation, forward and backward.
+//
+// Forward   [teacher entries] -> row list -> compact X -> logits + softmax
+//           statistics GEMM -> losses
+// Backward  [teacher entries] -> row list -> compact X -> per vocabulary
+//           piece: D GEMM, dX GEMM (fp32 sums), dW GEMM -> dX rounding
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <string>
+
+#include "head.h"
+#include "kernels.h"
+#include "moe.h"
+
+namespace {
+
+using namespace moe;
+
+constexpr int kMaxDevices = 64;
+constexpr bool kPairs = false;
+constexpr int64_t kPieceBytes = int64_t(256) << 20;   // default size of the D piece
+
+moe_status_t bad(const char* where, const char* what, moe_status_t s = MOE_ERR_INVALID_ARG) {
+  set_error_detail((std::string(where) + ": " + what).c_str());
+  return s;
+}
+moe_status_t cuda_bad(const char* where, const char* what, cudaError_t e) {
+  set_error_detail((std::string(where) + ": " + what + ": " + cudaGetErrorString(e)).c_str());
+  return MOE_ERR_CUDA;
+}
+
+struct DeviceFacts {
+  bool ready = false;
+  int sms = 0, pairs = 0;
+};
+DeviceFacts g_facts[kMaxDevices];
+std::mutex g_facts_mu;
+
+// Facts of the current device, and its context bound to the calling thread
+// (the tensor-map encoder is a driver call).
+moe_status_t device_facts(const char* where, DeviceFacts* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return cuda_bad(where, "no usable current device", e);
+  if (dev < 0 || dev >= kMaxDevices) return bad(where, "device ordinal out of range", MOE_ERR_UNSUPPORTED);
+  std::lock_guard<std::mutex> lock(g_facts_mu);
+  DeviceFacts& f = g_facts[dev];
+  if (!f.ready) {
+    int major = 0, minor = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (major != 10 || minor != 3)
+      return bad(where, "this library is built for sm_103a (GB300) only", MOE_ERR_UNSUPPORTED);
+    if ((e = cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+        (e = head_gemm_prepare()) != cudaSuccess || (e = head_gemm_max_pairs(&f.pairs)) != cudaSuccess)
+      return cuda_bad(where, "kernel attributes", e);
+    f.pairs = std::min(f.pairs, f.sms / 2);
+    if (f.pairs < 1) return bad(where, "no room for a CTA pair", MOE_ERR_CUDA);
+    f.ready = true;
+  }
+  *out = f;
+  return MOE_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// Row-major [rows, cols] with row stride ld (elements), box [box_r, box_c].
+bool tmap(CUtensorMap* m, const void* base, int esize, int64_t cols, int64_t rows, int64_t ld, int box_c, int box_r,
+          CUtensorMapSwizzle sw) {
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * esize};
+  cuuint32_t box[2] = {(cuuint32_t)box_c, (cuuint32_t)box_r};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+             const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool map_k(CUtensorMap* m, const void* b, int64_t cols, int64_t rows, int64_t ld, int box_r) {
+  return tmap(m, b, 2, cols, rows, ld, 64, box_r, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+struct Layout {
+  int64_t Tp, piece, ldl;   // padded rows, columns of one piece, leading dimension of the D piece
+  int K, nsplit;
+  bool pair;                // tiles of 256 token rows
+  size_t counts, scale, rowmap, inv, ids, probs, cnt, plogp, xc, part, zt, dl, acc, total;
+};
+
+// Tokens up to one CTA's 128 rows leave a pair's second half idle.
+bool use_pair(int64_t T) { return kPairs && T > 128; }
+
+Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, int pairs) {
+  Layout L{};
+  L.K = distill ? c.K : 1;
+  L.Tp = std::max<int64_t>(up(c.T, kHeadRowPad), kHeadRowPad);
+  L.pair = use_pair(c.T);
+  if (backward) {
+    int64_t p = c.piece > 0 ? up(c.piece, 256) : std::max<int64_t>(kPieceBytes / (2 * L.Tp), 8192);
+    const int64_t n = std::max<int64_t>(1, (up(c.V, 256) + p - 1) / p);
+    L.piece = up((c.V + n - 1) / n, 256);       // pieces of equal size
+    L.ldl = L.piece;
+    // dX tiles of one piece: split K until the tiles fill the SMs evenly.  In
+    // units of one 64-deep slice: whole waves of tiles, each with about 8
+    // slices of start and epilogue, and 2 per split for the sums' traffic.
+    const int rows = L.pair ? 256 : 128, workers = L.pair ? pairs : sms;
+    const int64_t tiles = (c.T + rows - 1) / rows * ((c.d + kHeadBN - 1) / kHeadBN);
+    const int64_t nkb = (std::min<int64_t>(L.piece, c.V) + 63) / 64;
+    double best = 0;
+    L.nsplit = 1;
+    for (int s = 1; s <= 16 && s <= nkb; ++s) {
+      const double cost = (double)((tiles * s + workers - 1) / workers) * ((double)nkb / s + 8) + 2.0 * s;
+      if (s == 1 || cost < best) {
+        best = cost;
+        L.nsplit = s;
+      }
+    }
+  }
+  size_t o = 0;
+  auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o += (bytes + 255) & ~size_t(255);
+    return at;
+  };
+  L.counts = take(16);
+  L.scale = take(4);
+  L.rowmap = take(L.Tp * 4);
+  L.inv = take(c.T * 4);
+  L.ids = take((size_t)c.T * L.K * 4);
+  L.probs = distill ? take((size_t)c.T * L.K * 4) : 0;
+  L.cnt = distill ? take(c.T * 4) : 0;
+  L.plogp = distill ? take(c.T * 4) : 0;
+  L.xc = take((size_t)L.Tp * c.d * 2);
+  if (!backward) {
+    L.part = take((size_t)((c.V + kHeadBN - 1) / kHeadBN) * 2 * L.Tp * 8);
+    L.zt = take((size_t)c.T * L.K * 4);
+  } else {
+    L.dl = take((size_t)L.Tp * L.ldl * 2);
+    L.acc = take((size_t)L.nsplit * L.Tp * c.d * 4);
+  }
+  L.total = o;
+  return L;
+}
+
+HeadRows rows_of(const Layout& L, void* ws, bool distill) {
+  char* b = static_cast<char*>(ws);
+  HeadRows r{};
+  r.n_active = reinterpret_cast<int32_t*>(b + L.counts);
+  r.scale = reinterpret_cast<float*>(b + L.scale);
+  r.rowmap = reinterpret_cast<int32_t*>(b + L.rowmap);
+  r.inv = reinterpret_cast<int32_t*>(b + L.inv);
+  r.ids = reinterpret_cast<int32_t*>(b + L.ids);
+  if (distill) {
+    r.probs = reinterpret_cast<float*>(b + L.probs);
+    r.cnt = reinterpret_cast<int32_t*>(b + L.cnt);
+    r.plogp = reinterpret_cast<float*>(b + L.plogp);
+  }
+  r.Xc = b + L.xc;
+  r.part = reinterpret_cast<float2*>(b + L.part);
+  r.zt = reinterpret_cast<float*>(b + L.zt);
+  r.dl = b + L.dl;
+  r.acc = reinterpret_cast<float*>(b + L.acc);
+  return r;
+}
+
+moe_status_t check_config(const char* where, const moe_head_config_t* c, bool distill) {
+  if (!c) return bad(where, "null config");
+  if (c->T < 0 || c->T > (1 << 20)) return bad(where, "T must be in [0, 2^20]");
+  if (c->V < 1 || c->V > (1 << 24)) return bad(where, "V must be in [1, 2^24]");
+  if (c->d < 8 || c->d > (1 << 16) || c->d % 8 != 0)
+    return bad(where, "d must be a multiple of 8 in [8, 2^16]", MOE_ERR_UNSUPPORTED);
+  if (distill && (c->K < 1 || c->K > kHeadMaxEntries)) return bad(where, "K must be in [1, 1024]");
+  if (distill && !(c->temperature > 0.0f && std::isfinite(c->temperature)))
+    return bad(where, "temperature must be positive and finite");
+  if (c->piece < 0 || c->piece > (1 << 24)) return bad(where, "piece must be in [0, 2^24]");
+  if (c->wait_timeout_ns < 0) return bad(where, "wait_timeout_ns must not be negative");
+  return MOE_OK;
+}
+
+bool ok_ptr(const void* p, unsigned align) { return p && (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0; }
+
+struct HeadCall {
+  const char* where;
+  const moe_head_config_t* cfg;
+  const void *X, *W, *labels, *teacher, *ids;   // labels, or teacher and ids
+  const float* dloss;                           // backward
+  const float* lse_in;
+  float *loss, *lse_out;
+  void *dX, *dW;
+  void* ws;
+  size_t ws_bytes;
+  int32_t* status;
+  cudaStream_t st;
+};
+
+moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
+  const char* w = h.where;
+  moe_status_t s = check_config(w, h.cfg, distill);
+  if (s != MOE_OK) return s;
+  const moe_head_config_t& c = *h.cfg;
+  const unsigned id_align = c.ids_int64 ? 8 : 4;
+  if (backward && h.dW && !ok_ptr(h.dW, 16)) return bad(w, "misaligned dW");
+  DeviceFacts f;
+  if (c.T == 0) {
+    if (backward && h.dW) {
+      if ((s = device_facts(w, &f)) != MOE_OK) return s;
+      const cudaError_t e = cudaMemsetAsync(h.dW, 0, (size_t)c.V * c.d * 2, h.st);
+      if (e != cudaSuccess) return cuda_bad(w, "memset of dW", e);
+    }
+    return MOE_OK;
+  }
+  if (!ok_ptr(h.X, 16) || !ok_ptr(h.W, 16)) return bad(w, "null or misaligned X or W");
+  if (distill ? (!ok_ptr(h.teacher, c.teacher_bf16 ? 2 : 4) || !ok_ptr(h.ids, id_align)) : !ok_ptr(h.labels, id_align))
+    return bad(w, "null or misaligned targets");
+  if (backward ? (!ok_ptr(h.dloss, 4) || !ok_ptr(h.lse_in, 4)) : (!ok_ptr(h.loss, 4) || !ok_ptr(h.lse_out, 4)))
+    return bad(w, "null or misaligned row vector");
+  if (backward && h.dX && !ok_ptr(h.dX, 16)) return bad(w, "misaligned dX");
+  if (backward && !h.dX && !h.dW) return MOE_OK;
+  if (!ok_ptr(h.ws, 256)) return bad(w, "null or misaligned workspace (256 bytes)");
+  if (h.status && !ok_ptr(h.status, 4)) return bad(w, "misaligned status");
+  if ((s = device_facts(w, &f)) != MOE_OK) return s;
+  const Layout L = layout(c, distill, backward, f.sms, f.pairs);
+  if (h.ws_bytes < L.total) return bad(w, "workspace smaller than moe_head_workspace_bytes");
+  const HeadRows r = rows_of(L, h.ws, distill);
+  const int T = (int)c.T;
+  const float temp = distill ? c.temperature : 1.0f;
+
+  HeadArgs a{};
+  a.n_active = r.n_active;
+  a.rowmap = r.rowmap;
+  a.ids = r.ids;
+  a.probs = r.probs;
+  a.cnt = r.cnt;
+  a.lse = h.lse_in;
+  a.dloss = h.dloss;
+  a.scale = r.scale;
+  a.part = r.part;
+  a.zt = r.zt;
+  a.status = h.status;
+  a.timeout_ns = c.wait_timeout_ns > 0 ? (uint64_t)c.wait_timeout_ns : 2000000000ull;
+  a.Tp = L.Tp;
+  a.V = c.V;
+  a.T = T;
+  a.d = c.d;
+  a.K = L.K;
+  a.nsplit = 1;
+  a.inv_temp = 1.0f / temp;
+  a.out_scale = temp;
+  a.stall = (c.debug_flags & MOE_DEBUG_STALL_TEST) ? 1 : 0;
+
+  const bool pw = kPairs;   // dW tiles: rows are vocabulary
+  const int brow = L.pair ? 128 : 256;
+  bool ok = map_k(&a.mapA0, h.X, c.d, T, c.d, 128) && map_k(&a.mapA1, r.Xc, c.d, L.Tp, c.d, 128) &&
+            map_k(&a.mapB0, h.W, c.d, c.V, c.d, brow);
+  HeadArgs ax{}, aw{};
+  if (backward) {
+    ok = ok && tmap(&a.mapO, r.dl, 2, L.ldl, L.Tp, L.ldl, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    ax = a;
+    ax.nsplit = L.nsplit;
+    ok = ok && map_k(&ax.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 128) && map_k(&ax.mapB0, h.W, c.d, c.V, c.d, 64) &&
+         tmap(&ax.mapO, r.acc, 4, c.d, (int64_t)L.nsplit * L.Tp, c.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    aw = a;
+    ok = ok && map_k(&aw.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 64) && map_k(&aw.mapB0, h.X, c.d, T, c.d, 64) &&
+         map_k(&aw.mapB1, r.Xc, c.d, L.Tp, c.d, 64);
+    if (h.dW) ok = ok && tmap(&aw.mapO, h.dW, 2, c.d, c.V, c.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
+  if (!ok) return bad(w, "tensor map encoding failed", MOE_ERR_CUDA);
+
+  (void)cudaGetLastError();   // an error read below belongs to these launches
+  cudaError_t e = cudaSuccess;
+  if (distill)
+    e = launch_head_entries(h.teacher, c.teacher_bf16 != 0, h.ids, c.ids_int64 != 0, T, L.K, c.V, a.inv_temp, r, h.st);
+  if (e == cudaSuccess) e = launch_head_scan(h.labels, c.ids_int64 != 0, h.dloss, T, c.V, r, h.st);
+  if (e == cudaSuccess) e = launch_head_gather(h.X, T, c.d, r, f.sms, h.st);
+  if (e != cudaSuccess) return cuda_bad(w, "row kernels", e);
+
+  const int64_t mt = (T + (L.pair ? 255 : 127)) / (L.pair ? 256 : 128);
+  auto grid = [&](bool pair, int64_t tiles) {
+    return (int)std::min<int64_t>(tiles, pair ? f.pairs : f.sms) * (pair ? 2 : 1);
+  };
+  if (!backward) {
+    const int64_t nt = (c.V + kHeadBN - 1) / kHeadBN;
+    a.v0 = 0;
+    a.vlen = c.V;
+    e = head_gemm_launch(kHeadLse, L.pair, a, grid(L.pair, mt * nt), h.st);
+    if (e == cudaSuccess)
+      e = launch_head_loss(T, L.K, (int)(2 * nt), L.Tp, temp, distill, r, h.loss, h.lse_out, h.st);
+    return e == cudaSuccess ? MOE_OK : cuda_bad(w, "launch", e);
+  }
+  const int64_t ntd = (c.d + kHeadBN - 1) / kHeadBN;
+  for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += L.piece) {
+    const int64_t vlen = std::min<int64_t>(L.piece, c.V - v0);
+    a.v0 = ax.v0 = aw.v0 = v0;
+    a.vlen = ax.vlen = aw.vlen = vlen;
+    ax.add = v0 > 0;
+    e = head_gemm_launch(kHeadDl, L.pair, a, grid(L.pair, mt * ((vlen + kHeadBN - 1) / kHeadBN)), h.st);
+    if (e == cudaSuccess && h.dX) {
+      // a short last piece may have fewer K slices than splits: the empty ones are zeros
+      e = head_gemm_launch(kHeadDX, L.pair, ax, grid(L.pair, mt * ntd * L.nsplit), h.st);
+    }
+    if (e == cudaSuccess && h.dW)
+      e = head_gemm_launch(kHeadDW, pw, aw, grid(pw, (vlen + (pw ? 255 : 127)) / (pw ? 256 : 128) * ntd), h.st);
+  }
+  if (e == cudaSuccess && h.dX) e = launch_head_dx(T, c.d, L.nsplit, L.Tp, temp, r, h.dX, f.sms, h.st);
+  return e == cudaSuccess ? MOE_OK : cuda_bad(w, "launch", e);
+}
+
+moe_status_t guarded(const HeadCall& h, bool distill, bool backward) {
+  try {
+    return run_head(h, distill, backward);
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_head_workspace_bytes(const moe_head_config_t* cfg, int32_t distill, int32_t backward, size_t* bytes) {
+  const char* w = "moe_head_workspace_bytes";
+  try {
+    if (!bytes) return bad(w, "null argument");
+    moe_status_t s = check_config(w, cfg, distill != 0);
+    if (s != MOE_OK) return s;
+    *bytes = 0;
+    if (cfg->T == 0) return MOE_OK;
+    DeviceFacts f;
+    if ((s = device_facts(w, &f)) != MOE_OK) return s;
+    *bytes = layout(*cfg, distill != 0, backward != 0, f.sms, f.pairs).total;
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+moe_status_t moe_cross_entropy_forward(const moe_head_config_t* cfg, const void* X, const void* W, const void* labels,
+                                       float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                                       int32_t* status, moe_stream_t stream) {
+  return guarded({"moe_cross_entropy_forward", cfg, X, W, labels, nullptr, nullptr, nullptr, nullptr, loss, lse,
+                  nullptr, nullptr, workspace, workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream)},
+                 false, false);
+}
+
+moe_status_t moe_cross_entropy_backward(const moe_head_config_t* cfg, const float* dloss, const void* X, const void* W,
+                                        const void* labels, const float* lse, void* dX, void* dW, void* workspace,
+                                        size_t workspace_bytes, int32_t* status, moe_stream_t stream) {
+  return guarded({"moe_cross_entropy_backward", cfg, X, W, labels, nullptr, nullptr, dloss, lse, nullptr, nullptr, dX,
+                  dW, workspace, workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream)},
+                 false, true);
+}
+
+moe_status_t moe_distill_forward(const moe_head_config_t* cfg, const void* X, const void* W, const void* teacher,
+                                 const void* ids, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                                 int32_t* status, moe_stream_t stream) {
+  return guarded({"moe_distill_forward", cfg, X, W, nullptr, teacher, ids, nullptr, nullptr, loss, lse, nullptr,
+                  nullptr, workspace, workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream)},
+                 true, false);
+}
+
+moe_status_t moe_distill_backward(const moe_head_config_t* cfg, const float* dloss, const void* X, const void* W,
+                                  const void* teacher, const void* ids, const float* lse, void* dX, void* dW,
+                                  void* workspace, size_t workspace_bytes, int32_t* status, moe_stream_t stream) {
+  return guarded({"moe_distill_backward", cfg, X, W, nullptr, teacher, ids, dloss, lse, nullptr, nullptr, dX, dW,
+                  workspace, workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream)},
+                 true, true);
+}
+
+}  // extern "C"

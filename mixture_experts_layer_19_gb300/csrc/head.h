@@ -1,0 +1,82 @@
+// head.h -- internal interface of the loss head (cross entropy and
+// distillation over logits = X W^T that are never stored whole): the GEMM
+// kinds of head_gemm.cuh and the row kernels of head_rows.cu, as head.cu
+// launches them.  Not part of the public ABI.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+constexpr int kHeadRowPad = 256;    // compact row buffers are padded to this many rows
+constexpr int kHeadBN = 256;        // vocabulary (or d) columns of one tile
+constexpr int kHeadMaxEntries = 1024;
+
+enum HeadKind { kHeadLse = 0, kHeadDl = 1, kHeadDX = 2, kHeadDW = 3 };
+
+// Arguments of one head GEMM launch.  "Compact" rows are the rows with a loss
+// (and, in the backward, a nonzero upstream gradient), in token order.
+struct HeadArgs {
+  CUtensorMap mapA0;         // A operand; X itself when every row is active
+  CUtensorMap mapA1;         // kHeadLse / kHeadDl: the compacted copy of X
+  CUtensorMap mapB0;         // B operand; kHeadDW: X itself
+  CUtensorMap mapB1;         // kHeadDW: the compacted copy of X
+  CUtensorMap mapO;          // stores: dl piece, fp32 dX sums, dW
+  const int32_t* n_active;   // [1] compact rows
+  const int32_t* rowmap;     // [Tp] token of each compact row
+  const int32_t* ids;        // [T, K] target entries of each token, ascending
+  const float* probs;        // [T, K] their probabilities, NULL = 1
+  const int32_t* cnt;        // [T] entries in use, NULL = K
+  const float* lse;          // kHeadDl: [T] saved log-sum-exp (of the logits over the temperature)
+  const float* dloss;        // kHeadDl: [T] upstream gradient
+  const float* scale;        // kHeadDl: [1] common factor of dloss; kHeadDW: the same, applied to the tile
+  float2* part;              // kHeadLse: [2 * NT, Tp] (max, sum of exp) of 128 columns of one row
+  float* zt;                 // kHeadLse: [T, K] logits at the target entries
+  int32_t* status;
+  uint64_t timeout_ns;
+  int64_t Tp;                // padded rows of the compact buffers
+  int64_t V;                 // vocabulary
+  int64_t v0, vlen;          // this piece of it (kHeadLse: 0, V)
+  int T, d, K;
+  int nsplit;                // kHeadDX: the vocabulary piece is split over this many tiles
+  int add;                   // kHeadDX: add into the fp32 sums (0: first piece, overwrite)
+  float inv_temp;            // 1 / temperature
+  float out_scale;           // kHeadDW: temperature, multiplied with *scale
+  int stall;                 // test hook: the producer issues nothing
+};
+
+cudaError_t head_gemm_prepare();
+// pair: two CTAs work on one 256-row tile (cta_group::2); otherwise one CTA on 128 rows.
+cudaError_t head_gemm_launch(int kind, bool pair, const HeadArgs& a, int grid, cudaStream_t st);
+cudaError_t head_gemm_max_pairs(int* pairs);
+
+// ---- row kernels (head_rows.cu)
+struct HeadRows {
+  int32_t* n_active;   // [4]
+  float* scale;        // [1] common factor of the upstream gradients (backward)
+  int32_t* rowmap;     // [Tp]
+  int32_t* inv;        // [T] compact row of each token, -1 = inactive
+  int32_t* ids;        // [T, K]
+  float* probs;        // [T, K] (distillation)
+  int32_t* cnt;        // [T]    (distillation)
+  float* plogp;        // [T]    (distillation, forward) sum p log p
+  void* Xc;            // [Tp, d] bf16
+  float2* part;        // [2 * NT, Tp]
+  float* zt;           // [T, K]
+  void* dl;            // [Tp, piece] bf16
+  float* acc;          // [S, Tp, d]
+};
+
+cudaError_t launch_head_entries(const void* teacher, bool teacher_bf16, const void* ids, bool ids64, int T, int K,
+                                int64_t V, float inv_temp, const HeadRows& r, cudaStream_t st);
+// labels != NULL: cross entropy (fills r.ids); otherwise r.cnt says which rows count.
+cudaError_t launch_head_scan(const void* labels, bool ids64, const float* dloss, int T, int64_t V, const HeadRows& r,
+                             cudaStream_t st);
+cudaError_t launch_head_gather(const void* X, int T, int d, const HeadRows& r, int num_sms, cudaStream_t st);
+cudaError_t launch_head_loss(int T, int K, int np, int64_t Tp, float temperature, bool distill, const HeadRows& r,
+                             float* loss, float* lse, cudaStream_t st);
+cudaError_t launch_head_dx(int T, int d, int nsplit, int64_t Tp, float out_scale, const HeadRows& r, void* dX,
+                           int num_sms, cudaStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,77 @@
+// head_gemm.cu -- instantiations and launches of the loss head's GEMMs.
+#include "head_gemm.cuh"
+
+namespace moe {
+
+namespace {
+
+template <int KIND, int CG>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(head_gemm_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              HeadTraits<KIND, CG>::smem_bytes);
+}
+
+template <int KIND, int CG>
+cudaError_t launch_one(const HeadArgs& a, int grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kHeadThreads);
+  cfg.dynamicSmemBytes = HeadTraits<KIND, CG>::smem_bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, head_gemm_kernel<KIND, CG>, a);
+}
+
+template <int CG>
+cudaError_t launch_kind(int kind, const HeadArgs& a, int grid, cudaStream_t st) {
+  switch (kind) {
+    case kHeadLse: return launch_one<kHeadLse, CG>(a, grid, st);
+    case kHeadDl: return launch_one<kHeadDl, CG>(a, grid, st);
+    case kHeadDX: return launch_one<kHeadDX, CG>(a, grid, st);
+    default: return launch_one<kHeadDW, CG>(a, grid, st);
+  }
+}
+
+template <int CG>
+cudaError_t prepare_kinds() {
+  cudaError_t e = prepare_one<kHeadLse, CG>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDl, CG>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDX, CG>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDW, CG>();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t head_gemm_prepare() {
+  cudaError_t e = prepare_kinds<1>();
+  return e == cudaSuccess ? prepare_kinds<2>() : e;
+}
+
+cudaError_t head_gemm_launch(int kind, bool pair, const HeadArgs& a, int grid, cudaStream_t st) {
+  return pair ? launch_kind<2>(kind, a, grid, st) : launch_kind<1>(kind, a, grid, st);
+}
+
+// How many CTA pairs the device holds at once: the static schedule's grid.
+cudaError_t head_gemm_max_pairs(int* pairs) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kHeadThreads);
+  cfg.dynamicSmemBytes = HeadTraits<kHeadDl, 2>::smem_bytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(pairs, head_gemm_kernel<kHeadDl, 2>, &cfg);
+}
+
+}  // namespace moe

@@ -1,0 +1,569 @@
+// head_gemm.cuh -- persistent tcgen05 GEMM of the loss head.
+//
+// With X [T, d] activations and W [V, d] the head's weight, logits z = X W^T
+// are computed tile by tile and consumed in the epilogue:
+//   kHeadLse  z tile -> per row (max, sum of exp) of 128 columns, and the
+//             logits at the row's target entries; nothing else leaves the SM
+//   kHeadDl   z tile again -> D = (softmax - target) * upstream, bf16, one
+//             piece of the vocabulary at a time
+//   kHeadDX   D . W      (K = vocabulary piece) into fp32 sums
+//   kHeadDW   D^T . X    (K = tokens), one bf16 rounding
+//
+// Roles per CTA (320 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA
+// issuer, warps 2..9 epilogue (two per TMEM lane quadrant, 128 columns each).
+// CG = 1: one CTA computes a 128 x 256 tile.  CG = 2: a pair of CTAs computes
+// 256 x 256; each holds its 128 rows of A and half of B's 256 columns, so an
+// SM fetches 32 KB instead of 48 KB per 64-deep slice of K.
+// Two TMEM accumulators of 256 columns overlap a tile's epilogue with the
+// next tile's products.  Tiles are handed out statically and every sum has
+// one fixed order: bitwise repeatable.
+//
+// The tensor cores add into fp32 accumulators with truncation, which pulls a
+// 7168-long dot product towards zero by about 7e-6 of its value (measured
+// against 64 bits).  The loss is a difference of logits, so kHeadLse ends an
+// accumulator every kLseChunk of K and adds the parts in registers, rounded
+// to nearest.  The gradients are rounded to bf16 and do not need it.
+#pragma once
+#include "head.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kHBM = 128;                    // rows per CTA
+constexpr int kHBK = 64;                     // K slice (128 bytes of bf16)
+constexpr int kHeadThreads = 320;
+constexpr int kHeadEpiWarps = 8;
+constexpr int kLseChunk = 16;                // K slices per accumulator of kHeadLse (1024)
+
+template <int KIND, int CG>
+struct HeadTraits {
+  static constexpr bool a_mn = KIND == kHeadDW;
+  static constexpr bool b_mn = KIND == kHeadDX || KIND == kHeadDW;
+  static constexpr int a_bytes = kHBM * kHBK * 2;             // 16 KB
+  static constexpr int b_rows = kHeadBN / CG;
+  static constexpr int b_bytes = b_rows * kHBK * 2;           // 32 / 16 KB
+  static constexpr int stage_bytes = a_bytes + b_bytes;
+  static constexpr int stages = CG == 2 ? 6 : 4;
+  // staging per epilogue warp: 32 x 32 bf16 twice, or 32 x 32 fp32 once
+  static constexpr int staging = KIND == kHeadLse ? 0 : 4096;
+  static constexpr int smem_bytes = stages * stage_bytes + kHeadEpiWarps * staging + 1024 + 256;
+};
+
+struct HeadTile {
+  int64_t row0;    // first row of the tile (compact rows, or vocabulary rows of the piece)
+  int64_t col0;    // first column (vocabulary inside the piece, or d)
+  int kb0, nkb;    // K slices
+  int split;
+};
+
+template <int KIND, int CG>
+__device__ __forceinline__ int64_t head_tiles(const HeadArgs& g, int na, int& MT, int& NT) {
+  constexpr int TM = kHBM * CG;
+  const int64_t mrows = KIND == kHeadDW ? g.vlen : na;
+  const int64_t ncols = (KIND == kHeadLse || KIND == kHeadDl) ? g.vlen : g.d;
+  MT = (int)((mrows + TM - 1) / TM);
+  NT = (int)((ncols + kHeadBN - 1) / kHeadBN);
+  return (int64_t)MT * NT * (KIND == kHeadDX ? g.nsplit : 1);
+}
+
+template <int KIND, int CG>
+__device__ __forceinline__ HeadTile head_tile(const HeadArgs& g, int na, int MT, int NT, int64_t w) {
+  HeadTile t;
+  t.split = 0;
+  int64_t mt, nt;
+  if (KIND == kHeadDW) {
+    // d tiles fastest: the piece's D^T block is read by neighbours, X stays in L2
+    mt = w / NT;
+    nt = w - mt * NT;
+  } else {
+    // row tiles fastest: a W tile is read by neighbours, X (or D) stays in L2
+    const int64_t per = (int64_t)MT * NT;
+    t.split = (int)(w / per);
+    const int64_t local = w - t.split * per;
+    nt = local / MT;
+    mt = local - nt * MT;
+  }
+  t.row0 = mt * (kHBM * CG);
+  t.col0 = nt * kHeadBN;
+  t.kb0 = 0;
+  if (KIND == kHeadDX) {
+    const int nkb = (int)((g.vlen + kHBK - 1) / kHBK);
+    const int base = nkb / g.nsplit, rem = nkb % g.nsplit;
+    t.nkb = base + (t.split < rem ? 1 : 0);
+    t.kb0 = t.split * base + min(t.split, rem);
+  } else {
+    t.nkb = ((KIND == kHeadDW ? na : g.d) + kHBK - 1) / kHBK;
+  }
+  return t;
+}
+
+// Accumulators (TMEM phases) of one tile, and the K slices of phase i.
+template <int KIND>
+__device__ __forceinline__ int head_phases(int nkb) {
+  return KIND == kHeadLse ? (nkb + kLseChunk - 1) / kLseChunk : 1;
+}
+
+// ---------------------------------------------------------------- pair (cta_group::2) pieces
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t mapa_u32(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m, int32_t x, int32_t y,
+                                                 uint32_t bar_cluster, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar_cluster), "l"(policy)
+      : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void head_tmem_alloc(uint32_t* slot) {
+  if constexpr (CG == 1) {
+    tmem_alloc(slot, 512);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void head_tmem_free(uint32_t taddr) {
+  if constexpr (CG == 1)
+    tmem_dealloc(taddr, 512);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void head_mma(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accum) {
+  if constexpr (CG == 1)
+    umma_bf16(d_tmem, ad, bd, idesc, accum);
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(accum)
+        : "memory");
+}
+// Arrive on `bar` of this CTA (and of its peer, CG = 2) once the MMAs issued so far completed.
+template <int CG>
+__device__ __forceinline__ void head_commit(uint64_t* bar) {
+  if constexpr (CG == 1)
+    umma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// TMA store / fp32 reduce of one staged 32 x 32 block.
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* m, const void* src, int32_t x, int32_t y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+// bf16 block for a 64-byte-swizzled store: 16-byte chunk c of row r at c ^ ((r >> 1) & 3).
+__device__ __forceinline__ void head_stage_bf16(uint8_t* buf, int lane, const float* v) {
+  const int sw = (lane >> 1) & 3;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ sw) << 4)) =
+        make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
+                   pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+}
+// fp32 block for a 128-byte-swizzled store: chunk c of row r at c ^ (r & 7).
+__device__ __forceinline__ void head_stage_f32(uint8_t* buf, int lane, const uint32_t* v) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+
+// First entry of an ascending list that is >= key.
+__device__ __forceinline__ int lower_bound_i32(const int32_t* a, int n, int64_t key) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)__ldg(a + mid) < key) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <int KIND, int CG>
+__global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid_constant__ HeadArgs g) {
+  using TR = HeadTraits<KIND, CG>;
+  constexpr int kSt = TR::stages;
+  extern __shared__ uint8_t smem_raw[];
+  // every CTA of a launch has the same dynamic shared-memory base, so a pair's layouts coincide
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* stage_base = smem;
+  uint8_t* staging_base = smem + kSt * TR::stage_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging_base + kHeadEpiWarps * TR::staging);
+  uint64_t* full = bars;                 // used in the leader CTA
+  uint64_t* empty = bars + kSt;
+  uint64_t* tfull = bars + 2 * kSt;
+  uint64_t* tempty = bars + 2 * kSt + 2; // used in the leader CTA
+  uint64_t* drain = bars + 2 * kSt + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kSt + 5);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSt; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], kHeadEpiWarps * CG);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&g.mapA0);
+    tma_prefetch_desc(&g.mapB0);
+  }
+  if (warp == 1) {
+    head_tmem_alloc<CG>(tmem_slot);
+    tc_fence_before();
+  }
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  WaitCtl wc{g.status, abort_flag, g.timeout_ns};
+
+  const int na = *g.n_active;
+  int MT, NT;
+  const int64_t nwork = head_tiles<KIND, CG>(g, na, MT, NT);
+  const int64_t w0 = blockIdx.x / CG;
+  const int64_t wstep = gridDim.x / CG;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      const uint64_t pol = policy_evict_last();
+      const bool all = na == g.T;                       // no row skipped: X is read in place
+      const CUtensorMap* mA = (KIND <= kHeadDl && !all) ? &g.mapA1 : &g.mapA0;
+      const CUtensorMap* mB = (KIND == kHeadDW && !all) ? &g.mapB1 : &g.mapB0;
+      uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int64_t w = w0; w < nwork && ok && !g.stall; w += wstep) {
+        const HeadTile t = head_tile<KIND, CG>(g, na, MT, NT, w);
+        const int64_t arow = t.row0 + rank * kHBM;          // this CTA's rows of A
+        const int64_t bcol = t.col0 + rank * TR::b_rows;    // and columns of B
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          if (!mbar_wait(&empty[s], ph ^ 1, wc)) { ok = false; break; }
+          if (leader) mbar_arrive_expect_tx(&full[s], TR::stage_bytes * CG);
+          uint8_t* sa = stage_base + s * TR::stage_bytes;
+          uint8_t* sb = sa + TR::a_bytes;
+          const int32_t k0 = (t.kb0 + kb) * kHBK;
+          const uint32_t bar_c = CG == 2 ? mapa_u32(smem_u32(&full[s]), 0) : 0;
+          auto load = [&](uint8_t* dst, const CUtensorMap* m, int64_t x, int64_t y) {
+            if constexpr (CG == 1) tma_load_2d(dst, m, (int32_t)x, (int32_t)y, &full[s], pol);
+            else tma_load_2d_pair(dst, m, (int32_t)x, (int32_t)y, bar_c, pol);
+          };
+          if (KIND == kHeadDW) {
+#pragma unroll
+            for (int j = 0; j < kHBM / 64; ++j) load(sa + j * 8192, mA, arow + j * 64, k0);
+          } else {
+            load(sa, mA, k0, arow);
+          }
+          if (KIND == kHeadDX || KIND == kHeadDW) {
+            const int64_t krow = (KIND == kHeadDX ? g.v0 : 0) + k0;
+#pragma unroll
+            for (int j = 0; j < TR::b_rows / 64; ++j) load(sb + j * 8192, mB, bcol + j * 64, krow);
+          } else {
+            load(sb, mB, k0, g.v0 + bcol);
+          }
+          issued |= 1u << s;
+          last_par = (last_par & ~(1u << s)) | (ph << s);
+          if (++s == kSt) { s = 0; ph ^= 1; }
+        }
+      }
+      if (!ok) {
+        // abort: give every issued copy time to land before the CTA may exit
+        // (the barriers are the leader's; its peer waits a fixed time)
+        const uint64_t t0 = globaltimer_ns();
+        if (leader) {
+          for (int st = 0; st < kSt; ++st) {
+            if (!(issued & (1u << st))) continue;
+            while (!mbar_try_wait(&full[st], (last_par >> st) & 1u))
+              if (globaltimer_ns() - t0 > 50000000ull) break;
+          }
+        } else {
+          while (globaltimer_ns() - t0 < 5000000ull) __nanosleep(1000);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idesc = idesc_bf16(kHBM * CG, kHeadBN, TR::a_mn ? 1 : 0, TR::b_mn ? 1 : 0);
+      uint32_t s = 0, ph = 0, acc = 0, aph = 0;
+      bool ok = true;
+      for (int64_t w = w0; w < nwork && ok; w += wstep) {
+        const HeadTile t = head_tile<KIND, CG>(g, na, MT, NT, w);
+        if (t.nkb == 0) continue;
+        const int phases = head_phases<KIND>(t.nkb);
+        for (int p = 0; p < phases && ok; ++p) {
+          const int k_lo = (int)((int64_t)t.nkb * p / phases), k_hi = (int)((int64_t)t.nkb * (p + 1) / phases);
+          if (!mbar_wait(&tempty[acc], aph ^ 1, wc)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + acc * kHeadBN;
+          for (int kb = k_lo; kb < k_hi; ++kb) {
+            if (!mbar_wait(&full[s], ph, wc)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(stage_base + s * TR::stage_bytes);
+            const uint32_t sb = sa + TR::a_bytes;
+#pragma unroll
+            for (int kk = 0; kk < kHBK / 16; ++kk) {
+              const uint64_t ad =
+                  TR::a_mn ? sdesc_sw128(sa + kk * 2048, 8192, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024);
+              const uint64_t bd =
+                  TR::b_mn ? sdesc_sw128(sb + kk * 2048, 8192, 1024) : sdesc_sw128(sb + kk * 32, 16, 1024);
+              head_mma<CG>(d_tmem, ad, bd, idesc, (kb > k_lo || kk) ? 1u : 0u);
+            }
+            head_commit<CG>(&empty[s]);
+            if (++s == kSt) { s = 0; ph ^= 1; }
+          }
+          if (!ok) break;
+          head_commit<CG>(&tfull[acc]);
+          acc ^= 1;
+          if (acc == 0) aph ^= 1;
+        }
+      }
+      if (!ok) {  // abort: let the products in flight finish before TMEM is freed
+        head_commit<CG>(drain);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0))
+          if (globaltimer_ns() - t0 > 50000000ull) break;
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3;                 // TMEM lane quadrant of this warp
+    const int h = (warp - 2) >> 2;          // column half
+    uint8_t* stg = staging_base + (warp - 2) * TR::staging;
+    uint32_t acc = 0, aph = 0;
+    uint32_t buf_ctr = 0;
+    const float c2 = g.inv_temp * 1.4426950408889634f;   // logits to base-2 exponents
+    auto release = [&](uint32_t a) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 1) mbar_arrive(&tempty[a]);
+        else mbar_arrive_cluster(mapa_u32(smem_u32(&tempty[a]), 0));
+      }
+    };
+    for (int64_t w = w0; w < nwork; w += wstep) {
+      const HeadTile t = head_tile<KIND, CG>(g, na, MT, NT, w);
+      const int64_t row = t.row0 + rank * kHBM + 32 * q + lane;   // this lane's row
+      const int64_t rowq = row - lane;                            // the warp's first row
+      const int64_t colh = t.col0 + h * 128;                      // the warp's first column
+      const uint32_t lane_off = (uint32_t)(32 * q) << 16;
+
+      if constexpr (KIND == kHeadLse || KIND == kHeadDl) {
+        const bool live = row < na;
+        const int64_t tok = live ? g.rowmap[row] : 0;
+        const int32_t* ids = g.ids + tok * g.K;
+        const int cnt = live ? (g.cnt ? g.cnt[tok] : g.K) : 0;
+        const int64_t vcol = g.v0 + colh;                         // vocabulary id of the first column
+        int e = lower_bound_i32(ids, cnt, vcol);
+        if constexpr (KIND == kHeadLse) {
+          float z[128];
+          const int phases = head_phases<KIND>(t.nkb);
+          bool ok = true;
+          for (int p = 0; p < phases; ++p) {
+            if (!mbar_wait(&tfull[acc], aph, wc)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * 128;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t r[32];
+              tmem_ld32(tb + c * 32, r);
+              tmem_ld_wait();
+              if (p == 0) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[c * 32 + i] = __uint_as_float(r[i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[c * 32 + i] += __uint_as_float(r[i]);
+              }
+            }
+            release(acc);
+            acc ^= 1;
+            if (acc == 0) aph ^= 1;
+          }
+          if (!ok) break;
+          // logits at this row's target entries inside these 128 columns
+          while (true) {
+            const int64_t id = e < cnt ? (int64_t)__ldg(ids + e) : INT64_MAX;
+            const bool hit = id < vcol + 128;
+            if (!__any_sync(0xffffffffu, hit)) break;
+            const int col = hit ? (int)(id - vcol) : -1;
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i == col) v = z[i];
+            if (hit) g.zt[tok * g.K + e] = v;
+            ++e;
+          }
+          const int64_t left = g.vlen - colh;
+          if (left < 128) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= left) z[i] = -INFINITY;
+          }
+          float m4[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+          for (int i = 4; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], z[i]);
+          const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          const float mb = m == -INFINITY ? 0.0f : m * c2;        // a block without columns sums to 0
+          float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s4[i & 3] += ex2_approx(fmaf(z[i], c2, -mb));
+          if (row < g.Tp)
+            g.part[(2 * (t.col0 / kHeadBN) + h) * g.Tp + row] =
+                make_float2(m * g.inv_temp, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+        } else {
+          const float rl = live ? g.lse[tok] * 1.4426950408889634f : 0.0f;
+          float gr = 0.0f;
+          if (live) gr = g.dloss[tok] / *g.scale;
+          if (!mbar_wait(&tfull[acc], aph, wc)) break;
+          tc_fence_after();
+          const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * 128;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tb + c * 32, r);
+            tmem_ld_wait();
+            if (c == 3) release(acc);
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = ex2_approx(fmaf(__uint_as_float(r[i]), c2, -rl));
+            while (true) {
+              const int64_t id = e < cnt ? (int64_t)__ldg(ids + e) : INT64_MAX;
+              const bool hit = id < vcol + c * 32 + 32;
+              if (!__any_sync(0xffffffffu, hit)) break;
+              const int col = hit ? (int)(id - vcol) - c * 32 : -1;
+              const float p = hit ? (g.probs ? __ldg(g.probs + tok * g.K + e) : 1.0f) : 0.0f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i == col) v[i] -= p;
+              if (hit) ++e;
+            }
+            const int64_t left = g.vlen - colh - c * 32;          // columns past the vocabulary are zeros
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = (live && i < left) ? v[i] * gr : 0.0f;
+            uint8_t* buf = stg + (buf_ctr & 1) * 2048;
+            ++buf_ctr;
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+            head_stage_bf16(buf, lane, v);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&g.mapO, buf, (int32_t)(colh + c * 32), (int32_t)rowq);
+              bulk_commit();
+            }
+          }
+          acc ^= 1;
+          if (acc == 0) aph ^= 1;
+        }
+      } else {
+        const bool has = t.nkb > 0;
+        if (has) {
+          if (!mbar_wait(&tfull[acc], aph, wc)) break;
+          tc_fence_after();
+        }
+        const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * 128;
+        const float sc = KIND == kHeadDW ? *g.scale * g.out_scale : 1.0f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          if (has) {
+            tmem_ld32(tb + c * 32, r);
+            tmem_ld_wait();
+            if (c == 3) release(acc);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
+          }
+          const int64_t col = colh + c * 32;
+          if constexpr (KIND == kHeadDX) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+            head_stage_f32(stg, lane, r);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && col < g.d && rowq < g.Tp) {
+              const int32_t y = (int32_t)(t.split * g.Tp + rowq);
+              if (g.add) tma_reduce_add_2d(&g.mapO, stg, (int32_t)col, y);
+              else tma_store_2d(&g.mapO, stg, (int32_t)col, y);
+              bulk_commit();
+            }
+          } else {
+            uint8_t* buf = stg + (buf_ctr & 1) * 2048;
+            ++buf_ctr;
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = has ? __uint_as_float(r[i]) * sc : 0.0f;
+            head_stage_bf16(buf, lane, v);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (col < g.d && rowq < g.vlen) tma_store_2d(&g.mapO, buf, (int32_t)col, (int32_t)(g.v0 + rowq));
+              bulk_commit();
+            }
+          }
+        }
+        if (has) {
+          acc ^= 1;
+          if (acc == 0) aph ^= 1;
+        }
+      }
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();   // no arrival or copy may target a CTA that has left
+  if (warp == 1) {
+    tc_fence_after();
+    head_tmem_free<CG>(tmem_base);
+  }
+}
+
+}  // namespace moe

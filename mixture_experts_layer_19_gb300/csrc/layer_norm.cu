@@ -1,0 +1,570 @@
+// layer_norm.cu -- layer norm forward and backward over row-major [rows, d].
+//
+// Bound by HBM: the forward reads x and writes y, the backward reads x and dy
+// and writes dx, each once.  A block keeps a whole row in registers (up to 16
+// elements per thread), so the two passes of the variance -- mean first, then
+// squares about it, which does not cancel as a difference of sums would --
+// cost no second read.  Blocks are persistent: the weights, and the
+// backward's column sums of dw and db, stay in registers from row to row, and
+// the next row's loads are in flight while the current one is reduced.  The
+// backward's per-block column sums go to workspace once per block and are
+// added in block order by a second kernel: no atomics, bitwise repeatable.
+// Rows longer than 8192 elements are read again instead of kept.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "kernels.h"
+#include "moe.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxThreads = 512;
+constexpr int kMaxElems = 16;          // elements of a row per thread
+
+template <class T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <class T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// VW elements of T moved as one access (16 bytes, or one element).
+template <class T, int VW>
+struct alignas(sizeof(T) * VW) Vec {
+  T v[VW];
+};
+
+// VW weights as fp32, in accesses of up to 16 bytes.
+template <class WT, int VW>
+__device__ __forceinline__ void load_weights(const WT* p, float (&o)[VW]) {
+  constexpr int N = VW * (int)sizeof(WT) > 16 ? 16 / (int)sizeof(WT) : VW;
+#pragma unroll
+  for (int k = 0; k < VW; k += N) {
+    const Vec<WT, N> q = *reinterpret_cast<const Vec<WT, N>*>(p + k);
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[k + i] = to_f(q.v[i]);
+  }
+}
+
+// Sum of NV values over the block, the same on every thread.  `buf` alternates
+// between calls so that one barrier per call is enough.
+template <int NV>
+__device__ __forceinline__ void block_sum(float (&s)[NV], float (*red)[NV], int nw) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+  if (nw == 1) return;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) red[warp][i] = s[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NV; ++i) s[i] = 0.0f;
+  for (int w = 0; w < nw; ++w)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] += red[w][i];
+}
+
+template <class XT, class WT, int VW, int VPT>
+__global__ void __launch_bounds__(kMaxThreads) ln_fwd_kernel(const XT* __restrict__ x, const WT* __restrict__ w,
+                                                             const WT* __restrict__ b, int64_t rows, int d, float eps,
+                                                             XT* __restrict__ y, float* __restrict__ mean,
+                                                             float* __restrict__ rstd) {
+  using V = Vec<XT, VW>;
+  __shared__ float red[2][16][1];
+  const int vecs = d / VW, nw = blockDim.x >> 5, tid = threadIdx.x;
+  const float inv_d = 1.0f / (float)d;
+  float wr[VPT][VW], br[VPT][VW];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = tid + j * blockDim.x;
+#pragma unroll
+    for (int i = 0; i < VW; ++i) wr[j][i] = br[j][i] = 0.0f;
+    if (c < vecs) {
+      load_weights<WT, VW>(w + c * VW, wr[j]);
+      if (b) load_weights<WT, VW>(b + c * VW, br[j]);
+    }
+  }
+  V nx[VPT];
+  int64_t r = blockIdx.x;
+  auto fetch = [&](int64_t row) {
+    const V* src = reinterpret_cast<const V*>(x + row * d);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = tid + j * blockDim.x;
+      if (c < vecs) nx[j] = src[c];
+    }
+  };
+  if (r < rows) fetch(r);
+  for (; r < rows; r += gridDim.x) {
+    float v[VPT][VW];
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const bool in = tid + j * blockDim.x < vecs;
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        v[j][i] = in ? to_f(nx[j].v[i]) : 0.0f;
+        s[0] += v[j][i];
+      }
+    }
+    if (r + gridDim.x < rows) fetch(r + gridDim.x);
+    block_sum<1>(s, red[0], nw);
+    const float m = s[0] * inv_d;
+    float q[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const bool in = tid + j * blockDim.x < vecs;
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        v[j][i] -= m;
+        if (in) q[0] = fmaf(v[j][i], v[j][i], q[0]);
+      }
+    }
+    block_sum<1>(q, red[1], nw);
+    const float rs = 1.0f / sqrtf(q[0] * inv_d + eps);
+    V* dst = reinterpret_cast<V*>(y + r * d);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = tid + j * blockDim.x;
+      if (c < vecs) {
+        V o;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) o.v[i] = from_f<XT>(fmaf(v[j][i] * rs, wr[j][i], br[j][i]));
+        dst[c] = o;
+      }
+    }
+    if (tid == 0) {
+      mean[r] = m;
+      rstd[r] = rs;
+    }
+  }
+}
+
+template <class XT, class WT, int VW, int VPT>
+__global__ void __launch_bounds__(kMaxThreads) ln_bwd_kernel(const XT* __restrict__ dy, const XT* __restrict__ x,
+                                                             const WT* __restrict__ w, const float* __restrict__ mean,
+                                                             const float* __restrict__ rstd, int64_t rows, int d,
+                                                             XT* __restrict__ dx, float* __restrict__ part_w,
+                                                             float* __restrict__ part_b) {
+  using V = Vec<XT, VW>;
+  __shared__ float red[2][16][2];
+  const int vecs = d / VW, nw = blockDim.x >> 5, tid = threadIdx.x;
+  const float inv_d = 1.0f / (float)d;
+  float wr[VPT][VW], aw[VPT][VW], ab[VPT][VW];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = tid + j * blockDim.x;
+#pragma unroll
+    for (int i = 0; i < VW; ++i) wr[j][i] = aw[j][i] = ab[j][i] = 0.0f;
+    if (c < vecs) load_weights<WT, VW>(w + c * VW, wr[j]);
+  }
+  V nx[VPT], ng[VPT];
+  float nm = 0.0f, nr = 0.0f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+#pragma unroll
+    for (int i = 0; i < VW; ++i) nx[j].v[i] = ng[j].v[i] = from_f<XT>(0.0f);
+  auto fetch = [&](int64_t row) {
+    const V* sx = reinterpret_cast<const V*>(x + row * d);
+    const V* sg = reinterpret_cast<const V*>(dy + row * d);
+    nm = mean[row];
+    nr = rstd[row];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = tid + j * blockDim.x;
+      if (c < vecs) {
+        nx[j] = sx[c];
+        ng[j] = sg[c];
+      }
+    }
+  };
+  int64_t r = blockIdx.x;
+  int flip = 0;
+  if (r < rows) fetch(r);
+  for (; r < rows; r += gridDim.x) {
+    V cx[VPT], cg[VPT];
+    const float m = nm, rs = nr;
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      cx[j] = nx[j];
+      cg[j] = ng[j];
+      const bool in = tid + j * blockDim.x < vecs;
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        const float n = (to_f(cx[j].v[i]) - m) * rs, g = to_f(cg[j].v[i]);
+        const float gw = g * wr[j][i];
+        if (in) {
+          s[0] += gw;
+          s[1] = fmaf(gw, n, s[1]);
+          aw[j][i] = fmaf(g, n, aw[j][i]);
+          ab[j][i] += g;
+        }
+      }
+    }
+    if (r + gridDim.x < rows) fetch(r + gridDim.x);
+    if (!dx) continue;
+    block_sum<2>(s, red[flip], nw);
+    flip ^= 1;
+    const float c1 = s[0] * inv_d, c2 = s[1] * inv_d;
+    V* dst = reinterpret_cast<V*>(dx + r * d);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int c = tid + j * blockDim.x;
+      if (c < vecs) {
+        V o;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+          const float n = (to_f(cx[j].v[i]) - m) * rs;
+          o.v[i] = from_f<XT>(rs * (to_f(cg[j].v[i]) * wr[j][i] - c1 - n * c2));
+        }
+        dst[c] = o;
+      }
+    }
+  }
+  if (!part_w) return;
+  const int64_t base = (int64_t)blockIdx.x * d;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = tid + j * blockDim.x;
+    if (c < vecs)
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        part_w[base + c * VW + i] = aw[j][i];
+        part_b[base + c * VW + i] = ab[j][i];
+      }
+  }
+}
+
+// dw / db[c] = sum of the G per-block sums, in an order fixed by G: 32 slices
+// of blocks, each in order, then the slices in order.  Block = 32 columns.
+template <class WT>
+__global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__ part_w,
+                                                       const float* __restrict__ part_b, int G, int d,
+                                                       WT* __restrict__ dw, WT* __restrict__ db) {
+  __shared__ float sw[32][33], sb[32][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float a = 0.0f, b = 0.0f;
+  if (c < d)
+    for (int g = slice; g < G; g += 32) {
+      a += part_w[(int64_t)g * d + c];
+      b += part_b[(int64_t)g * d + c];
+    }
+  sw[slice][lane] = a;
+  sb[slice][lane] = b;
+  __syncthreads();
+  if (slice < 2 && c < d) {
+    float s = 0.0f;
+    for (int i = 0; i < 32; ++i) s += slice ? sb[i][lane] : sw[i][lane];
+    WT* out = slice ? db : dw;
+    if (out) out[c] = from_f<WT>(s);
+  }
+}
+
+// ---- rows that do not fit the registers: the row is read once per pass
+template <class XT, class WT>
+__global__ void __launch_bounds__(512) ln_fwd_long_kernel(const XT* __restrict__ x, const WT* __restrict__ w,
+                                                          const WT* __restrict__ b, int64_t rows, int64_t d, float eps,
+                                                          XT* __restrict__ y, float* __restrict__ mean,
+                                                          float* __restrict__ rstd) {
+  __shared__ float red[2][16][1];
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const XT* src = x + r * d;
+    float s[1] = {0.0f}, q[1] = {0.0f};
+    for (int64_t c = threadIdx.x; c < d; c += 512) s[0] += to_f(src[c]);
+    block_sum<1>(s, red[0], 16);
+    const float m = s[0] / (float)d;
+    for (int64_t c = threadIdx.x; c < d; c += 512) {
+      const float v = to_f(src[c]) - m;
+      q[0] = fmaf(v, v, q[0]);
+    }
+    block_sum<1>(q, red[1], 16);
+    const float rs = 1.0f / sqrtf(q[0] / (float)d + eps);
+    for (int64_t c = threadIdx.x; c < d; c += 512)
+      y[r * d + c] = from_f<XT>(fmaf((to_f(src[c]) - m) * rs, to_f(w[c]), b ? to_f(b[c]) : 0.0f));
+    if (threadIdx.x == 0) {
+      mean[r] = m;
+      rstd[r] = rs;
+    }
+  }
+}
+
+template <class XT, class WT>
+__global__ void __launch_bounds__(512) ln_bwd_long_kernel(const XT* __restrict__ dy, const XT* __restrict__ x,
+                                                          const WT* __restrict__ w, const float* __restrict__ mean,
+                                                          const float* __restrict__ rstd, int64_t rows, int64_t d,
+                                                          XT* __restrict__ dx) {
+  __shared__ float red[2][16][2];
+  int flip = 0;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const XT *sx = x + r * d, *sg = dy + r * d;
+    const float m = mean[r], rs = rstd[r];
+    float s[2] = {0.0f, 0.0f};
+    for (int64_t c = threadIdx.x; c < d; c += 512) {
+      const float gw = to_f(sg[c]) * to_f(w[c]);
+      s[0] += gw;
+      s[1] = fmaf(gw, (to_f(sx[c]) - m) * rs, s[1]);
+    }
+    block_sum<2>(s, red[flip], 16);
+    flip ^= 1;
+    const float c1 = s[0] / (float)d, c2 = s[1] / (float)d;
+    for (int64_t c = threadIdx.x; c < d; c += 512)
+      dx[r * d + c] = from_f<XT>(rs * (to_f(sg[c]) * to_f(w[c]) - c1 - (to_f(sx[c]) - m) * rs * c2));
+  }
+}
+
+// Column sums of one slice of rows: thread = column, blockIdx.y = slice.
+template <class XT>
+__global__ void __launch_bounds__(256) ln_bwd_long_cols_kernel(const XT* __restrict__ dy, const XT* __restrict__ x,
+                                                               const float* __restrict__ mean,
+                                                               const float* __restrict__ rstd, int64_t rows, int64_t d,
+                                                               float* __restrict__ part_w, float* __restrict__ part_b) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= d) return;
+  const int64_t lo = rows * blockIdx.y / gridDim.y, hi = rows * (blockIdx.y + 1) / gridDim.y;
+  float a = 0.0f, b = 0.0f;
+  for (int64_t r = lo; r < hi; ++r) {
+    const float g = to_f(dy[r * d + c]);
+    a = fmaf(g, (to_f(x[r * d + c]) - mean[r]) * rstd[r], a);
+    b += g;
+  }
+  part_w[blockIdx.y * d + c] = a;
+  part_b[blockIdx.y * d + c] = b;
+}
+
+// ---------------------------------------------------------------- host side
+struct Shape {
+  bool reg;        // the row fits the registers
+  int vw, vpt, threads;
+};
+
+// Elements per access: 16 bytes when every row starts on a 16-byte boundary,
+// else one.  Accesses per thread: the fewest (a power of two) that cover the row
+// with 512 threads.
+Shape shape_of(int64_t d, int esize) {
+  Shape s{};
+  s.vw = (d * esize) % 16 == 0 ? 16 / esize : 1;
+  const int64_t vecs = d / s.vw;
+  for (s.vpt = 1; s.vpt * s.vw <= kMaxElems; s.vpt *= 2)
+    if ((vecs + s.vpt - 1) / s.vpt <= kMaxThreads) {
+      s.reg = true;
+      s.threads = (int)(((vecs + s.vpt - 1) / s.vpt + 31) / 32 * 32);
+      return s;
+    }
+  return s;
+}
+
+int current_sms() {
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return std::max(1, sms);
+}
+
+// Blocks of the persistent kernels; the backward's number of column partials.
+int64_t fwd_blocks(int64_t rows, const Shape& s, int sms) {
+  return std::min<int64_t>(rows, (int64_t)sms * std::max(1, std::min(16, 2048 / s.threads)));
+}
+int64_t bwd_blocks(int64_t rows, int threads, int sms) {
+  return std::min<int64_t>(rows, (int64_t)sms * std::max(1, std::min(8, 512 / threads)));
+}
+int64_t long_slices(int64_t rows) { return std::min<int64_t>(rows, 32); }
+
+template <class XT, class WT, int VW, int VPT>
+cudaError_t fwd_go(const void* x, const void* w, const void* b, int64_t rows, int d, float eps, void* y, float* mean,
+                   float* rstd, const Shape& s, int sms, cudaStream_t st) {
+  ln_fwd_kernel<XT, WT, VW, VPT><<<(unsigned)fwd_blocks(rows, s, sms), s.threads, 0, st>>>(
+      (const XT*)x, (const WT*)w, (const WT*)b, rows, d, eps, (XT*)y, mean, rstd);
+  return cudaGetLastError();
+}
+template <class XT, class WT, int VW, int VPT>
+cudaError_t bwd_go(const void* dy, const void* x, const void* w, const float* mean, const float* rstd, int64_t rows,
+                   int d, void* dx, float* pw, float* pb, const Shape& s, int64_t blocks, cudaStream_t st) {
+  ln_bwd_kernel<XT, WT, VW, VPT><<<(unsigned)blocks, s.threads, 0, st>>>(
+      (const XT*)dy, (const XT*)x, (const WT*)w, mean, rstd, rows, d, (XT*)dx, pw, pb);
+  return cudaGetLastError();
+}
+
+// Calls GO<XT, WT, VW, VPT>(args...) for the shape's access width and count.
+#define LN_DISPATCH(GO, ...)                                                  \
+  do {                                                                        \
+    constexpr int kFull = 16 / (int)sizeof(XT);                               \
+    if (s.vw == kFull) {                                                      \
+      if (s.vpt == 1) return GO<XT, WT, kFull, 1>(__VA_ARGS__);               \
+      if (s.vpt == 2) return GO<XT, WT, kFull, 2>(__VA_ARGS__);               \
+      return GO<XT, WT, kFull, kMaxElems / kFull>(__VA_ARGS__);               \
+    }                                                                         \
+    if (s.vpt <= 2) return GO<XT, WT, 1, 2>(__VA_ARGS__);                     \
+    if (s.vpt <= 4) return GO<XT, WT, 1, 4>(__VA_ARGS__);                     \
+    if (s.vpt <= 8) return GO<XT, WT, 1, 8>(__VA_ARGS__);                     \
+    return GO<XT, WT, 1, 16>(__VA_ARGS__);                                    \
+  } while (0)
+
+template <class XT, class WT>
+cudaError_t fwd_types(const void* x, const void* w, const void* b, int64_t rows, int64_t d, float eps, void* y,
+                      float* mean, float* rstd, cudaStream_t st) {
+  const Shape s = shape_of(d, sizeof(XT));
+  const int sms = current_sms();
+  if (s.reg) LN_DISPATCH(fwd_go, x, w, b, rows, (int)d, eps, y, mean, rstd, s, sms, st);
+  ln_fwd_long_kernel<XT, WT><<<(unsigned)std::min<int64_t>(rows, 4 * sms), 512, 0, st>>>(
+      (const XT*)x, (const WT*)w, (const WT*)b, rows, d, eps, (XT*)y, mean, rstd);
+  return cudaGetLastError();
+}
+
+template <class XT, class WT>
+cudaError_t bwd_rows(const void* dy, const void* x, const void* w, const float* mean, const float* rstd, int64_t rows,
+                     int64_t d, void* dx, float* pw, float* pb, const Shape& s, int64_t blocks, cudaStream_t st) {
+  if (s.reg) LN_DISPATCH(bwd_go, dy, x, w, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
+  cudaError_t e = cudaSuccess;
+  if (dx) {
+    ln_bwd_long_kernel<XT, WT><<<(unsigned)std::min<int64_t>(rows, 4 * current_sms()), 512, 0, st>>>(
+        (const XT*)dy, (const XT*)x, (const WT*)w, mean, rstd, rows, d, (XT*)dx);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess && pw) {
+    ln_bwd_long_cols_kernel<XT><<<dim3((unsigned)((d + 255) / 256), (unsigned)blocks), 256, 0, st>>>(
+        (const XT*)dy, (const XT*)x, mean, rstd, rows, d, pw, pb);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+int64_t partials_of(int64_t rows, int64_t d, int esize, int sms) {
+  const Shape s = shape_of(d, esize);
+  return s.reg ? bwd_blocks(rows, s.threads, sms) : long_slices(rows);
+}
+
+template <class XT, class WT>
+cudaError_t bwd_types(const void* dy, const void* x, const void* w, const float* mean, const float* rstd, int64_t rows,
+                      int64_t d, void* dx, void* dw, void* db, float* ws, cudaStream_t st) {
+  const Shape s = shape_of(d, sizeof(XT));
+  const int64_t G = partials_of(rows, d, sizeof(XT), current_sms());
+  const bool sums = dw || db;
+  float* pw = sums ? ws : nullptr;
+  float* pb = sums ? ws + G * d : nullptr;
+  cudaError_t e = bwd_rows<XT, WT>(dy, x, w, mean, rstd, rows, d, dx, pw, pb, s, G, st);
+  if (e != cudaSuccess || !sums) return e;
+  ln_cols_kernel<WT><<<(unsigned)((d + 31) / 32), 1024, 0, st>>>(pw, pb, (int)G, (int)d, (WT*)dw, (WT*)db);
+  return cudaGetLastError();
+}
+
+moe_status_t bad(const char* where, const char* what) {
+  set_error_detail((std::string(where) + ": " + what).c_str());
+  return MOE_ERR_INVALID_ARG;
+}
+moe_status_t done(const char* where, cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  set_error_detail((std::string(where) + ": launch: " + cudaGetErrorString(e)).c_str());
+  return MOE_ERR_CUDA;
+}
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool sizes_ok(int64_t rows, int64_t d) {
+  return rows >= 0 && d >= 1 && d <= (1 << 20) && rows <= ((int64_t)1 << 40) / d;
+}
+
+size_t workspace_of(int64_t rows, int64_t d) {
+  if (rows == 0) return 0;
+  const int sms = current_sms();
+  const int64_t G = std::max(partials_of(rows, d, 2, sms), partials_of(rows, d, 4, sms));
+  return (size_t)G * 2 * d * 4;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_layer_norm_forward(const void* x, const void* w, const void* b, int64_t rows, int64_t d,
+                                    int32_t x_f32, int32_t w_f32, float eps, void* y, float* mean, float* rstd,
+                                    moe_stream_t stream) {
+  const char* where = "moe_layer_norm_forward";
+  try {
+    if (!sizes_ok(rows, d)) return bad(where, "need rows >= 0, 1 <= d <= 2^20 and rows * d <= 2^40");
+    if (!(eps >= 0.0f && std::isfinite(eps))) return bad(where, "eps must be finite and not negative");
+    if (rows == 0) return MOE_OK;
+    if (!x || !w || !y || !mean || !rstd) return bad(where, "null pointer");
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+      return bad(where, "misaligned pointer (tensors 16 bytes)");
+    (void)cudaGetLastError();
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    using bf = __nv_bfloat16;
+    if (x_f32)
+      return done(where, w_f32 ? fwd_types<float, float>(x, w, b, rows, d, eps, y, mean, rstd, st)
+                               : fwd_types<float, bf>(x, w, b, rows, d, eps, y, mean, rstd, st));
+    return done(where, w_f32 ? fwd_types<bf, float>(x, w, b, rows, d, eps, y, mean, rstd, st)
+                             : fwd_types<bf, bf>(x, w, b, rows, d, eps, y, mean, rstd, st));
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+moe_status_t moe_layer_norm_workspace_bytes(int64_t rows, int64_t d, size_t* bytes) {
+  const char* where = "moe_layer_norm_workspace_bytes";
+  try {
+    if (!bytes) return bad(where, "null argument");
+    if (!sizes_ok(rows, d)) return bad(where, "need rows >= 0, 1 <= d <= 2^20 and rows * d <= 2^40");
+    *bytes = workspace_of(rows, d);
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* w, const float* mean,
+                                     const float* rstd, int64_t rows, int64_t d, int32_t x_f32, int32_t w_f32,
+                                     void* dx, void* dw, void* db, void* workspace, size_t workspace_bytes,
+                                     moe_stream_t stream) {
+  const char* where = "moe_layer_norm_backward";
+  try {
+    if (!sizes_ok(rows, d)) return bad(where, "need rows >= 0, 1 <= d <= 2^20 and rows * d <= 2^40");
+    if (!aligned(dx, 16) || !aligned(dw, 16) || !aligned(db, 16)) return bad(where, "misaligned output (16 bytes)");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    (void)cudaGetLastError();
+    if (rows == 0) {
+      cudaError_t e = cudaSuccess;
+      const size_t n = (size_t)d * (w_f32 ? 4 : 2);
+      if (dw) e = cudaMemsetAsync(dw, 0, n, st);
+      if (e == cudaSuccess && db) e = cudaMemsetAsync(db, 0, n, st);
+      return done(where, e);
+    }
+    if (!dy || !x || !w || !mean || !rstd) return bad(where, "null pointer");
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(mean, 4) || !aligned(rstd, 4))
+      return bad(where, "misaligned pointer (tensors 16 bytes)");
+    if (!dx && !dw && !db) return MOE_OK;
+    if (dw || db) {
+      if (!workspace || !aligned(workspace, 256)) return bad(where, "null or misaligned workspace (256 bytes)");
+      if (workspace_bytes < workspace_of(rows, d))
+        return bad(where, "workspace smaller than moe_layer_norm_workspace_bytes");
+    }
+    float* ws = static_cast<float*>(workspace);
+    using bf = __nv_bfloat16;
+    if (x_f32)
+      return done(where, w_f32 ? bwd_types<float, float>(dy, x, w, mean, rstd, rows, d, dx, dw, db, ws, st)
+                               : bwd_types<float, bf>(dy, x, w, mean, rstd, rows, d, dx, dw, db, ws, st));
+    return done(where, w_f32 ? bwd_types<bf, float>(dy, x, w, mean, rstd, rows, d, dx, dw, db, ws, st)
+                             : bwd_types<bf, bf>(dy, x, w, mean, rstd, rows, d, dx, dw, db, ws, st));
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+}  // extern "C"

@@ -39,7 +39,10 @@ EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_saved_bytes", "moe_forward", "m
             "moe_status_string", "moe_last_error", "moe_route_noalloc", "moe_quantize_weights",
             "moe_mx_quantize", "moe_router_forward", "moe_router_backward", "moe_mx_quantize_transposed",
             "moe_plan_info", "moe_nv_tensor_scale", "moe_nv_quantize", "moe_nv_quantize_transposed",
-            "moe_nv_weight_scales", "moe_debug_quant_dump", "moe_plan_padded_rows")
+            "moe_nv_weight_scales", "moe_debug_quant_dump", "moe_plan_padded_rows",
+            "moe_layer_norm_forward", "moe_layer_norm_workspace_bytes", "moe_layer_norm_backward",
+            "moe_head_workspace_bytes", "moe_cross_entropy_forward", "moe_cross_entropy_backward",
+            "moe_distill_forward", "moe_distill_backward")
 
 
 class moe_config_t(ctypes.Structure):
@@ -50,11 +53,18 @@ class moe_config_t(ctypes.Structure):
                 ("debug_flags", ctypes.c_uint32), ("device", ctypes.c_int32), ("ep_ranks", ctypes.c_int32)]
 
 
+class moe_head_config_t(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("V", ctypes.c_int64), ("d", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("temperature", ctypes.c_float), ("ids_int64", ctypes.c_int32), ("teacher_bf16", ctypes.c_int32),
+                ("piece", ctypes.c_int64), ("wait_timeout_ns", ctypes.c_int64), ("debug_flags", ctypes.c_uint32)]
+
+
 def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"libmoe.so not built ({path}); run __graft_entry__.build() first")
     lib = ctypes.CDLL(path)
     P, I64, I32, VP, FP = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p
+    HC = ctypes.POINTER(moe_head_config_t)
     sig = {
         "moe_plan": [ctypes.POINTER(moe_config_t), ctypes.POINTER(P)],
         "moe_plan_destroy": [P],
@@ -81,6 +91,14 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         "moe_nv_weight_scales": [P, FP, P],
         "moe_debug_quant_dump": [P, I32, FP, VP, VP, P],
         "moe_plan_padded_rows": [P, ctypes.POINTER(I64)],
+        "moe_layer_norm_forward": [VP, VP, VP, I64, I64, I32, I32, ctypes.c_float, VP, FP, FP, P],
+        "moe_layer_norm_workspace_bytes": [I64, I64, ctypes.POINTER(ctypes.c_size_t)],
+        "moe_layer_norm_backward": [VP, VP, VP, FP, FP, I64, I64, I32, I32, VP, VP, VP, VP, ctypes.c_size_t, P],
+        "moe_head_workspace_bytes": [HC, I32, I32, ctypes.POINTER(ctypes.c_size_t)],
+        "moe_cross_entropy_forward": [HC, VP, VP, VP, FP, FP, VP, ctypes.c_size_t, VP, P],
+        "moe_cross_entropy_backward": [HC, FP, VP, VP, VP, FP, VP, VP, VP, ctypes.c_size_t, VP, P],
+        "moe_distill_forward": [HC, VP, VP, VP, VP, FP, FP, VP, ctypes.c_size_t, VP, P],
+        "moe_distill_backward": [HC, FP, VP, VP, VP, VP, FP, VP, VP, VP, ctypes.c_size_t, VP, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
