@@ -22,7 +22,7 @@ namespace {
 using namespace moe;
 
 constexpr int kMaxDevices = 64;
-constexpr bool kPairs = false;
+
 constexpr int64_t kPieceBytes = int64_t(256) << 20;   // default size of the D piece
 
 moe_status_t bad(const char* where, const char* what, moe_status_t s = MOE_ERR_INVALID_ARG) {
@@ -107,7 +107,7 @@ struct Layout {
 };
 
 // Tokens up to one CTA's 128 rows leave a pair's second half idle.
-bool use_pair(int64_t T) { return kPairs && T > 128; }
+bool use_pair(int64_t T) { return T > 128; }
 
 Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, int pairs) {
   Layout L{};
@@ -267,7 +267,7 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   a.out_scale = temp;
   a.stall = (c.debug_flags & MOE_DEBUG_STALL_TEST) ? 1 : 0;
 
-  const bool pw = kPairs;   // dW tiles: rows are vocabulary
+  const bool pw = true;   // dW tiles: rows are vocabulary
   const int brow = L.pair ? 128 : 256;
   bool ok = map_k(&a.mapA0, h.X, c.d, T, c.d, 128) && map_k(&a.mapA1, r.Xc, c.d, L.Tp, c.d, 128) &&
             map_k(&a.mapB0, h.W, c.d, c.V, c.d, brow);

@@ -1,15 +1,20 @@
 // layer_norm.cu -- layer norm forward and backward over row-major [rows, d].
 //
 // Bound by HBM: the forward reads x and writes y, the backward reads x and dy
-// and writes dx, each once.  A block keeps a whole row in registers (up to 16
-// elements per thread), so the two passes of the variance -- mean first, then
-// squares about it, which does not cancel as a difference of sums would --
-// cost no second read.  Blocks are persistent: the weights, and the
-// backward's column sums of dw and db, stay in registers from row to row, and
-// the next row's loads are in flight while the current one is reduced.  The
-// backward's per-block column sums go to workspace once per block and are
-// added in block order by a second kernel: no atomics, bitwise repeatable.
-// Rows longer than 8192 elements are read again instead of kept.
+// and writes dx, each once.  A row stays in registers from its only read to
+// its result, so the two passes of the variance -- mean first, then squares
+// about it, which does not cancel as a difference of sums would -- cost no
+// second read.
+//   many rows, forward   one to four warps per row, the row packed in up to 28
+//                        16-byte registers vectors per lane, weights in shared
+//                        memory; with one warp there is no barrier at all
+//   few rows, odd widths one block per row
+//   backward             one block per row pair; each thread keeps its columns'
+//                        sums of dw and db in registers over all its rows and
+//                        prefetches later rows into its own shared memory
+//   rows past 8192 elements are read again instead of kept
+// The backward's per-block column sums go to workspace once per block and are
+// added in a fixed order by a second kernel: no atomics, bitwise repeatable.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -152,6 +157,342 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_kernel(const XT* __restric
       mean[r] = m;
       rstd[r] = rs;
     }
+  }
+}
+
+// ---------------------------------------------------------------- packed fp32 pairs
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_get(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Pair p of a 16-byte vector of XT: 4 pairs of bf16 or 2 of fp32.
+template <class XT>
+struct Pairs;
+template <>
+struct Pairs<__nv_bfloat16> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ f2 get(const uint4& v, int p) {
+    const uint32_t u = p == 0 ? v.x : p == 1 ? v.y : p == 2 ? v.z : v.w;
+    return f2_make(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void set(uint4& v, int p, f2 x) {
+    const float2 f = f2_get(x);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+    if (p == 0) v.x = u;
+    else if (p == 1) v.y = u;
+    else if (p == 2) v.z = u;
+    else v.w = u;
+  }
+};
+template <>
+struct Pairs<float> {
+  static constexpr int n = 2;
+  static __device__ __forceinline__ f2 get(const uint4& v, int p) {
+    return p == 0 ? f2_make(__uint_as_float(v.x), __uint_as_float(v.y))
+                  : f2_make(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  static __device__ __forceinline__ void set(uint4& v, int p, f2 x) {
+    const float2 f = f2_get(x);
+    if (p == 0) {
+      v.x = __float_as_uint(f.x);
+      v.y = __float_as_uint(f.y);
+    } else {
+      v.z = __float_as_uint(f.x);
+      v.w = __float_as_uint(f.y);
+    }
+  }
+};
+// Makes the packed row opaque between passes: the compiler would otherwise
+// keep every element's fp32 form from pass to pass, twice the registers.
+template <int NV>
+__device__ __forceinline__ void keep_packed(uint4 (&v)[NV]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) asm volatile("" : "+r"(v[j].x), "+r"(v[j].y), "+r"(v[j].z), "+r"(v[j].w));
+}
+__device__ __forceinline__ float weight_at(const void* w, bool f32, int i) {
+  return f32 ? reinterpret_cast<const float*>(w)[i] : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[i]);
+}
+
+// ---------------------------------------------------------------- forward, many rows
+// wpr warps per row, 12 / wpr rows per block at a time.  Shared memory holds
+// (w, w, b, b) of each pair of columns, plane by plane so that neighbouring
+// lanes read neighbouring 16 bytes.
+constexpr int kRowWarps = 12;
+template <class XT, int NV>
+__global__ void __launch_bounds__(kRowWarps * 32, 1) ln_fwd_rows_kernel(const uint4* __restrict__ x, const void* w,
+                                                                       const void* b, bool w_f32, int64_t rows, int d,
+                                                                       int wpr, float eps, uint4* __restrict__ y,
+                                                                       float* __restrict__ mean,
+                                                                       float* __restrict__ rstd) {
+  using P = Pairs<XT>;
+  extern __shared__ float4 wb[];                         // [P::n][vecs]
+  __shared__ float red[2][kRowWarps];
+  const int vecs = d / (2 * P::n);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < vecs * P::n; i += kRowWarps * 32) {
+    const int c = i / P::n, p = i - c * P::n, e = 2 * i;
+    wb[p * vecs + c] = make_float4(weight_at(w, w_f32, e), weight_at(w, w_f32, e + 1), b ? weight_at(b, w_f32, e) : 0.0f,
+                                   b ? weight_at(b, w_f32, e + 1) : 0.0f);
+  }
+  __syncthreads();
+  const int group = warp / wpr, gw = warp - group * wpr, groups = kRowWarps / wpr;
+  const int tid = gw * 32 + lane, nt = wpr * 32;
+  const float inv_d = 1.0f / (float)d;
+  // sum over the row's warps, in warp order, the same on every lane
+  auto row_sum = [&](float s, float* buf) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (wpr > 1) {
+      if (lane == 0) buf[warp] = s;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(nt) : "memory");
+      s = 0.0f;
+      for (int i = 0; i < wpr; ++i) s += buf[group * wpr + i];
+    }
+    return s;
+  };
+  for (int64_t r = (int64_t)blockIdx.x * groups + group; r < rows; r += (int64_t)gridDim.x * groups) {
+    const uint4* src = x + r * vecs;
+    uint4 v[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * nt;
+      v[j] = c < vecs ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
+    }
+    f2 s2 = 0, t2 = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int p = 0; p < P::n; p += 2) {
+        s2 = f2_add(s2, P::get(v[j], p));
+        t2 = f2_add(t2, P::get(v[j], p + 1));
+      }
+    keep_packed<NV>(v);
+    float2 s = f2_get(f2_add(s2, t2));
+    const float m = row_sum(s.x + s.y, red[0]) * inv_d;
+    const f2 mm = f2_make(-m, -m);
+    s2 = t2 = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (tid + j * nt < vecs) {
+#pragma unroll
+        for (int p = 0; p < P::n; p += 2) {
+          const f2 a = f2_add(P::get(v[j], p), mm), c = f2_add(P::get(v[j], p + 1), mm);
+          s2 = f2_fma(a, a, s2);
+          t2 = f2_fma(c, c, t2);
+        }
+      }
+    keep_packed<NV>(v);
+    s = f2_get(f2_add(s2, t2));
+    const float rs = 1.0f / sqrtf(row_sum(s.x + s.y, red[1]) * inv_d + eps);
+    const f2 rr = f2_make(rs, rs);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = tid + j * nt;
+      if (c < vecs) {
+        uint4 o;
+#pragma unroll
+        for (int p = 0; p < P::n; ++p) {
+          const float4 q = wb[p * vecs + c];
+          P::set(o, p, f2_fma(f2_mul(f2_add(P::get(v[j], p), mm), rr), f2_make(q.x, q.y), f2_make(q.z, q.w)));
+        }
+        __stcs(y + r * vecs + c, o);
+      }
+    }
+    if (tid == 0) {
+      mean[r] = m;
+      rstd[r] = rs;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+// Sums of four values over the block, the same on every thread.
+__device__ __forceinline__ void block_sum4(float (&s)[4], float4* red, int nw) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // lane l of a quad ends with value l: 2 + 1 exchanges instead of 4 sums of 2 steps
+  const bool b0 = lane & 1, b1 = lane & 2;
+  float a = b0 ? s[1] : s[0], c = b0 ? s[3] : s[2];
+  a += __shfl_xor_sync(0xffffffffu, b0 ? s[0] : s[1], 1);
+  c += __shfl_xor_sync(0xffffffffu, b0 ? s[2] : s[3], 1);
+  float e = b1 ? c : a;
+  e += __shfl_xor_sync(0xffffffffu, b1 ? a : c, 2);
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+  if (lane < 4) reinterpret_cast<float*>(red + warp)[lane] = e;
+  __syncthreads();
+  f2 p = 0, q = 0;
+  for (int w = 0; w < nw; ++w) {
+    const float4 v = red[w];
+    p = f2_add(p, f2_make(v.x, v.y));
+    q = f2_add(q, f2_make(v.z, v.w));
+  }
+  const float2 x = f2_get(p), y = f2_get(q);
+  s[0] = x.x;
+  s[1] = x.y;
+  s[2] = y.x;
+  s[3] = y.y;
+}
+
+// Two rows per step, `depth` (even) rows prefetched with cp.async.  A thread
+// reads from shared memory only what it copied there itself, so the copies
+// need no barrier; the one per step is the reduction's.
+template <class XT, int VPT>
+__global__ void __launch_bounds__(kMaxThreads, 1) ln_bwd_rows_kernel(
+    const uint4* __restrict__ dy, const uint4* __restrict__ x, const void* w, bool w_f32,
+    const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows, int d, int depth,
+    uint4* __restrict__ dx, float* __restrict__ part_w, float* __restrict__ part_b) {
+  using P = Pairs<XT>;
+  extern __shared__ uint4 ring[];                        // [depth][2][vecs]
+  __shared__ float4 red[2][16];
+  const int vecs = d / (2 * P::n), nw = blockDim.x >> 5, tid = threadIdx.x;
+  const float inv_d = 1.0f / (float)d;
+  f2 wr[VPT][P::n], aw[VPT][P::n], ab[VPT][P::n];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = tid + j * blockDim.x;
+#pragma unroll
+    for (int p = 0; p < P::n; ++p) {
+      const int e = c * 2 * P::n + 2 * p;
+      wr[j][p] = c < vecs ? f2_make(weight_at(w, w_f32, e), weight_at(w, w_f32, e + 1)) : 0;
+      aw[j][p] = ab[j][p] = 0;
+    }
+  }
+  const int64_t mine = (rows - blockIdx.x + gridDim.x - 1) / gridDim.x;    // rows blockIdx.x + k * gridDim.x
+  auto fetch = [&](int64_t k, int slot) {
+    if (k < mine) {
+      const int64_t base = ((int64_t)blockIdx.x + k * gridDim.x) * vecs;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int c = tid + j * blockDim.x;
+        if (c < vecs) {
+          cp_async16(ring + (2 * slot) * vecs + c, x + base + c);
+          cp_async16(ring + (2 * slot + 1) * vecs + c, dy + base + c);
+        }
+      }
+    }
+  };
+  for (int k = 0; k < depth; k += 2) {
+    fetch(k, k);
+    fetch(k + 1, k + 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  int slot = 0, flip = 0;
+  for (int64_t k = 0; k < mine; k += 2) {
+    float m[2], rs[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t r = (int64_t)blockIdx.x + (k + u) * gridDim.x;
+      m[u] = k + u < mine ? __ldg(mean + r) : 0.0f;
+      rs[u] = k + u < mine ? __ldg(rstd + r) : 0.0f;
+    }
+    // the pair of rows copied longest ago has landed
+    if (depth >= 8) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (depth == 6) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (depth == 4) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    uint4 vx[2][VPT], vg[2][VPT];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int c = tid + j * blockDim.x;
+        const bool in = c < vecs && k + u < mine;
+        vx[u][j] = in ? ring[(2 * (slot + u)) * vecs + c] : make_uint4(0, 0, 0, 0);
+        vg[u][j] = in ? ring[(2 * (slot + u) + 1) * vecs + c] : make_uint4(0, 0, 0, 0);
+      }
+    fetch(k + depth, slot);
+    fetch(k + depth + 1, slot + 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    slot = slot + 2 == depth ? 0 : slot + 2;
+    float s[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const f2 rr = f2_make(rs[u], rs[u]), mm = f2_make(-m[u], -m[u]);
+      f2 s0 = 0, s1 = 0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int p = 0; p < P::n; ++p) {
+          // columns past the row have dy = 0 and add nothing
+          const f2 n = f2_mul(f2_add(P::get(vx[u][j], p), mm), rr), g = P::get(vg[u][j], p);
+          const f2 gw = f2_mul(g, wr[j][p]);
+          s0 = f2_add(s0, gw);
+          s1 = f2_fma(gw, n, s1);
+          aw[j][p] = f2_fma(g, n, aw[j][p]);
+          ab[j][p] = f2_add(ab[j][p], g);
+        }
+      const float2 a = f2_get(s0), c = f2_get(s1);
+      s[2 * u] = a.x + a.y;
+      s[2 * u + 1] = c.x + c.y;
+    }
+    if (!dx) continue;
+    keep_packed<VPT>(vx[0]);
+    keep_packed<VPT>(vx[1]);
+    keep_packed<VPT>(vg[0]);
+    keep_packed<VPT>(vg[1]);
+    block_sum4(s, red[flip], nw);
+    flip ^= 1;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (k + u >= mine) break;
+      const f2 rr = f2_make(rs[u], rs[u]), mm = f2_make(-m[u], -m[u]);
+      const float c1 = -s[2 * u] * inv_d, c2 = -s[2 * u + 1] * inv_d;
+      const f2 k1 = f2_make(c1, c1), k2 = f2_make(c2, c2);
+      const int64_t base = ((int64_t)blockIdx.x + (k + u) * gridDim.x) * vecs;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int c = tid + j * blockDim.x;
+        if (c < vecs) {
+          uint4 o;
+#pragma unroll
+          for (int p = 0; p < P::n; ++p) {
+            const f2 n = f2_mul(f2_add(P::get(vx[u][j], p), mm), rr);
+            const f2 t = f2_fma(P::get(vg[u][j], p), wr[j][p], k1);
+            P::set(o, p, f2_mul(rr, f2_fma(n, k2, t)));
+          }
+          __stcs(dx + base + c, o);
+        }
+      }
+    }
+  }
+  if (!part_w) return;
+  const int64_t base = (int64_t)blockIdx.x * d;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = tid + j * blockDim.x;
+    if (c < vecs)
+#pragma unroll
+      for (int p = 0; p < P::n; ++p) {
+        *reinterpret_cast<float2*>(part_w + base + c * 2 * P::n + 2 * p) = f2_get(aw[j][p]);
+        *reinterpret_cast<float2*>(part_b + base + c * 2 * P::n + 2 * p) = f2_get(ab[j][p]);
+      }
   }
 }
 
@@ -401,7 +742,56 @@ cudaError_t bwd_go(const void* dy, const void* x, const void* w, const float* me
   return cudaGetLastError();
 }
 
+// Forward over many rows: the fewest warps per row (1, 2, 4) whose lanes hold
+// it in 28 vectors, and how many vectors that takes.  0 warps: not possible.
+struct RowPlan {
+  int wpr, nv;
+};
+RowPlan row_plan(int64_t d, int esize) {
+  if ((d * esize) % 16 != 0) return {0, 0};
+  const int64_t vecs = d * esize / 16;
+  for (int wpr = 1; wpr <= 4; wpr *= 2) {
+    const int64_t nv = (vecs + 32 * wpr - 1) / (32 * wpr);
+    if (nv <= 28) return {wpr, (int)nv};
+  }
+  return {0, 0};
+}
+
+template <class XT, int NV>
+cudaError_t fwd_rows_go(const void* x, const void* w, const void* b, bool w_f32, int64_t rows, int d, int wpr,
+                        float eps, void* y, float* mean, float* rstd, int sms, cudaStream_t st) {
+  const int smem = d * 8;
+  auto kernel = ln_fwd_rows_kernel<XT, NV>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t groups = kRowWarps / wpr;
+  kernel<<<(unsigned)std::min<int64_t>((rows + groups - 1) / groups, sms), kRowWarps * 32, smem, st>>>(
+      (const uint4*)x, w, b, w_f32, rows, d, wpr, eps, (uint4*)y, mean, rstd);
+  return cudaGetLastError();
+}
+
+template <class XT, int VPT>
+cudaError_t bwd_rows_go(const void* dy, const void* x, const void* w, bool w_f32, const float* mean, const float* rstd,
+                        int64_t rows, int d, void* dx, float* pw, float* pb, const Shape& s, int64_t blocks,
+                        cudaStream_t st) {
+  const int pair = 2 * 2 * d * (int)sizeof(XT);          // two rows of x and dy
+  const int depth = 2 * std::max(1, std::min(4, (200 << 10) / pair / std::max(1, std::min(8, 512 / s.threads))));
+  auto kernel = ln_bwd_rows_kernel<XT, VPT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, depth / 2 * pair);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)blocks, s.threads, depth / 2 * pair, st>>>((const uint4*)dy, (const uint4*)x, w, w_f32, mean, rstd,
+                                                               rows, d, depth, (uint4*)dx, pw, pb);
+  return cudaGetLastError();
+}
+
 // Calls GO<XT, WT, VW, VPT>(args...) for the shape's access width and count.
+#define LN_SCALAR(GO, ...)                                                    \
+  do {                                                                        \
+    if (s.vpt <= 2) return GO<XT, WT, 1, 2>(__VA_ARGS__);                     \
+    if (s.vpt <= 4) return GO<XT, WT, 1, 4>(__VA_ARGS__);                     \
+    if (s.vpt <= 8) return GO<XT, WT, 1, 8>(__VA_ARGS__);                     \
+    return GO<XT, WT, 1, 16>(__VA_ARGS__);                                    \
+  } while (0)
 #define LN_DISPATCH(GO, ...)                                                  \
   do {                                                                        \
     constexpr int kFull = 16 / (int)sizeof(XT);                               \
@@ -410,10 +800,7 @@ cudaError_t bwd_go(const void* dy, const void* x, const void* w, const float* me
       if (s.vpt == 2) return GO<XT, WT, kFull, 2>(__VA_ARGS__);               \
       return GO<XT, WT, kFull, kMaxElems / kFull>(__VA_ARGS__);               \
     }                                                                         \
-    if (s.vpt <= 2) return GO<XT, WT, 1, 2>(__VA_ARGS__);                     \
-    if (s.vpt <= 4) return GO<XT, WT, 1, 4>(__VA_ARGS__);                     \
-    if (s.vpt <= 8) return GO<XT, WT, 1, 8>(__VA_ARGS__);                     \
-    return GO<XT, WT, 1, 16>(__VA_ARGS__);                                    \
+    LN_SCALAR(GO, __VA_ARGS__);                                               \
   } while (0)
 
 template <class XT, class WT>
@@ -421,6 +808,15 @@ cudaError_t fwd_types(const void* x, const void* w, const void* b, int64_t rows,
                       float* mean, float* rstd, cudaStream_t st) {
   const Shape s = shape_of(d, sizeof(XT));
   const int sms = current_sms();
+  const RowPlan p = row_plan(d, sizeof(XT));
+  // many rows: enough to give every SM's 12 warps work; few are split over a block each instead
+  if (p.wpr && rows * p.wpr >= (int64_t)sms * kRowWarps) {
+    const bool wf = sizeof(WT) == 4;
+    if (p.nv <= 4) return fwd_rows_go<XT, 4>(x, w, b, wf, rows, (int)d, p.wpr, eps, y, mean, rstd, sms, st);
+    if (p.nv <= 8) return fwd_rows_go<XT, 8>(x, w, b, wf, rows, (int)d, p.wpr, eps, y, mean, rstd, sms, st);
+    if (p.nv <= 16) return fwd_rows_go<XT, 16>(x, w, b, wf, rows, (int)d, p.wpr, eps, y, mean, rstd, sms, st);
+    return fwd_rows_go<XT, 28>(x, w, b, wf, rows, (int)d, p.wpr, eps, y, mean, rstd, sms, st);
+  }
   if (s.reg) LN_DISPATCH(fwd_go, x, w, b, rows, (int)d, eps, y, mean, rstd, s, sms, st);
   ln_fwd_long_kernel<XT, WT><<<(unsigned)std::min<int64_t>(rows, 4 * sms), 512, 0, st>>>(
       (const XT*)x, (const WT*)w, (const WT*)b, rows, d, eps, (XT*)y, mean, rstd);
@@ -430,7 +826,14 @@ cudaError_t fwd_types(const void* x, const void* w, const void* b, int64_t rows,
 template <class XT, class WT>
 cudaError_t bwd_rows(const void* dy, const void* x, const void* w, const float* mean, const float* rstd, int64_t rows,
                      int64_t d, void* dx, float* pw, float* pb, const Shape& s, int64_t blocks, cudaStream_t st) {
-  if (s.reg) LN_DISPATCH(bwd_go, dy, x, w, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
+  if (s.reg && s.vw > 1) {
+    const bool wf = sizeof(WT) == 4;
+    if (s.vpt == 1) return bwd_rows_go<XT, 1>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
+    if (s.vpt == 2) return bwd_rows_go<XT, 2>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
+    return bwd_rows_go<XT, kMaxElems * (int)sizeof(XT) / 16>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s,
+                                                            blocks, st);
+  }
+  if (s.reg) LN_SCALAR(bwd_go, dy, x, w, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
   cudaError_t e = cudaSuccess;
   if (dx) {
     ln_bwd_long_kernel<XT, WT><<<(unsigned)std::min<int64_t>(rows, 4 * current_sms()), 512, 0, st>>>(
