@@ -2,10 +2,10 @@
 // workspace layout, tensor maps and the kernel sequence of cross entropy and
 // distillation, forward and backward.
 //
-// Forward   [teacher entries] -> row list -> compact X -> logits + softmax
+// Forward   [teacher entries] -> row list, compact X -> logits + softmax
 //           statistics GEMM -> losses
-// Backward  [teacher entries] -> row list -> compact X -> per vocabulary
-//           piece: D GEMM, dX GEMM (fp32 sums), dW GEMM -> dX rounding
+// Backward  [teacher entries] -> row list, compact X -> per vocabulary piece:
+//           D GEMM, dX GEMM (fp32 sums), dW GEMM -> dX rounding
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -102,39 +102,57 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 struct Layout {
   int64_t Tp, piece, ldl;   // padded rows, columns of one piece, leading dimension of the D piece
   int K, nsplit;
-  bool pair;                // tiles of 256 token rows
+  bool pair_z, pair_x, pair_w;   // CTA pairs for the logits, dX and dW products
+  bool sums;                // dX needs the fp32 sums (several pieces or splits)
   size_t counts, scale, rowmap, inv, ids, probs, cnt, plogp, xc, part, zt, dl, acc, total;
 };
 
-// Tokens up to one CTA's 128 rows leave a pair's second half idle.
-bool use_pair(int64_t T) { return T > 128; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Time of one product in units of one K slice of a pair's 256 x 256 tile
+// (0.27 us at 1.9 GHz): whole waves of tiles, each as long as its nkb slices or
+// its epilogue (epi slices, overlapped with the next tile's products), and the last
+// epilogue, which nothing overlaps.  A single CTA's slice moves 48 KB into its SM
+// where a pair moves 32 per SM, and takes 1.1 times as long (4096 x 7168 x
+// 65536 forward: 2508 us against 2393).
+constexpr double kEpiLogits = 12, kEpiGrad = 6, kStart = 16;
+double tiles_cost(int64_t m, int64_t ncols, double nkb, double epi, int splits, bool pair, int sms, int pairs) {
+  const int64_t tiles = ceil_div(m, pair ? 256 : 128) * ceil_div(ncols, kHeadBN) * splits;
+  return (double)ceil_div(tiles, pair ? pairs : sms) * std::max((pair ? 1.0 : 1.1) * nkb, epi) + kStart;
+}
+bool better_as_pair(int64_t m, int64_t ncols, double nkb, double epi, int sms, int pairs) {
+  return tiles_cost(m, ncols, nkb, epi, 1, true, sms, pairs) <= tiles_cost(m, ncols, nkb, epi, 1, false, sms, pairs);
+}
 
 Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, int pairs) {
   Layout L{};
   L.K = distill ? c.K : 1;
   L.Tp = std::max<int64_t>(up(c.T, kHeadRowPad), kHeadRowPad);
-  L.pair = use_pair(c.T);
+  L.nsplit = 1;
   if (backward) {
     int64_t p = c.piece > 0 ? up(c.piece, 256) : std::max<int64_t>(kPieceBytes / (2 * L.Tp), 8192);
-    const int64_t n = std::max<int64_t>(1, (up(c.V, 256) + p - 1) / p);
-    L.piece = up((c.V + n - 1) / n, 256);       // pieces of equal size
+    const int64_t n = std::max<int64_t>(1, ceil_div(up(c.V, 256), p));
+    L.piece = up(ceil_div(c.V, n), 256);        // pieces of equal size
     L.ldl = L.piece;
-    // dX tiles of one piece: split K until the tiles fill the SMs evenly.  In
-    // units of one 64-deep slice: whole waves of tiles, each with about 8
-    // slices of start and epilogue, and 2 per split for the sums' traffic.
-    const int rows = L.pair ? 256 : 128, workers = L.pair ? pairs : sms;
-    const int64_t tiles = (c.T + rows - 1) / rows * ((c.d + kHeadBN - 1) / kHeadBN);
-    const int64_t nkb = (std::min<int64_t>(L.piece, c.V) + 63) / 64;
+    const int64_t cols = std::min<int64_t>(L.piece, c.V);
+    // dX has few tiles when T is small: its K, the piece, is split until they
+    // fill the SMs; a split costs the traffic of its fp32 sums (about 2 slices)
+    const int64_t nkb = ceil_div(cols, 64);
     double best = 0;
-    L.nsplit = 1;
-    for (int s = 1; s <= 16 && s <= nkb; ++s) {
-      const double cost = (double)((tiles * s + workers - 1) / workers) * ((double)nkb / s + 8) + 2.0 * s;
-      if (s == 1 || cost < best) {
-        best = cost;
-        L.nsplit = s;
+    for (int pair = 0; pair < 2; ++pair)
+      for (int s = 1; s <= 16 && s <= nkb; ++s) {
+        const double cost = tiles_cost(c.T, c.d, (double)nkb / s, kEpiGrad, s, pair != 0, sms, pairs) + 2.0 * (s - 1);
+        if ((s == 1 && !pair) || cost < best) {
+          best = cost;
+          L.nsplit = s;
+          L.pair_x = pair != 0;
+        }
       }
-    }
+    L.pair_w = better_as_pair(cols, c.d, (double)ceil_div(c.T, 64), kEpiGrad, sms, pairs);
+    L.sums = L.nsplit > 1 || L.piece < c.V;
   }
+  L.pair_z = better_as_pair(c.T, backward ? std::min<int64_t>(L.piece, c.V) : c.V, (double)ceil_div(c.d, 64),
+                            kEpiLogits, sms, pairs);
   size_t o = 0;
   auto take = [&o](size_t bytes) {
     const size_t at = o;
@@ -155,7 +173,7 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
     L.zt = take((size_t)c.T * L.K * 4);
   } else {
     L.dl = take((size_t)L.Tp * L.ldl * 2);
-    L.acc = take((size_t)L.nsplit * L.Tp * c.d * 4);
+    L.acc = L.sums ? take((size_t)L.nsplit * L.Tp * c.d * 4) : 0;
   }
   L.total = o;
   return L;
@@ -267,21 +285,21 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   a.out_scale = temp;
   a.stall = (c.debug_flags & MOE_DEBUG_STALL_TEST) ? 1 : 0;
 
-  const bool pw = true;   // dW tiles: rows are vocabulary
-  const int brow = L.pair ? 128 : 256;
   bool ok = map_k(&a.mapA0, h.X, c.d, T, c.d, 128) && map_k(&a.mapA1, r.Xc, c.d, L.Tp, c.d, 128) &&
-            map_k(&a.mapB0, h.W, c.d, c.V, c.d, brow);
+            map_k(&a.mapB0, h.W, c.d, c.V, c.d, L.pair_z ? 128 : 256);
   HeadArgs ax{}, aw{};
   if (backward) {
-    ok = ok && tmap(&a.mapO, r.dl, 2, L.ldl, L.Tp, L.ldl, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    ok = ok && tmap(&a.mapO, r.dl, 2, L.ldl, L.Tp, L.ldl, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     ax = a;
     ax.nsplit = L.nsplit;
-    ok = ok && map_k(&ax.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 128) && map_k(&ax.mapB0, h.W, c.d, c.V, c.d, 64) &&
-         tmap(&ax.mapO, r.acc, 4, c.d, (int64_t)L.nsplit * L.Tp, c.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    ax.acc = r.acc;
+    ok = ok && map_k(&ax.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 128) && map_k(&ax.mapB0, h.W, c.d, c.V, c.d, 64);
+    if (L.sums)
+      ok = ok && tmap(&ax.mapO, r.acc, 4, c.d, (int64_t)L.nsplit * L.Tp, c.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     aw = a;
     ok = ok && map_k(&aw.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 64) && map_k(&aw.mapB0, h.X, c.d, T, c.d, 64) &&
          map_k(&aw.mapB1, r.Xc, c.d, L.Tp, c.d, 64);
-    if (h.dW) ok = ok && tmap(&aw.mapO, h.dW, 2, c.d, c.V, c.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (h.dW) ok = ok && tmap(&aw.mapO, h.dW, 2, c.d, c.V, c.d, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (!ok) return bad(w, "tensor map encoding failed", MOE_ERR_CUDA);
 
@@ -289,38 +307,37 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   cudaError_t e = cudaSuccess;
   if (distill)
     e = launch_head_entries(h.teacher, c.teacher_bf16 != 0, h.ids, c.ids_int64 != 0, T, L.K, c.V, a.inv_temp, r, h.st);
-  if (e == cudaSuccess) e = launch_head_scan(h.labels, c.ids_int64 != 0, h.dloss, T, c.V, r, h.st);
-  if (e == cudaSuccess) e = launch_head_gather(h.X, T, c.d, r, f.sms, h.st);
+  if (e == cudaSuccess)
+    e = launch_head_prep(h.labels, c.ids_int64 != 0, h.dloss, h.X, T, c.d, c.V, r, backward ? h.dX : nullptr, f.sms,
+                         h.st);
   if (e != cudaSuccess) return cuda_bad(w, "row kernels", e);
 
-  const int64_t mt = (T + (L.pair ? 255 : 127)) / (L.pair ? 256 : 128);
-  auto grid = [&](bool pair, int64_t tiles) {
-    return (int)std::min<int64_t>(tiles, pair ? f.pairs : f.sms) * (pair ? 2 : 1);
+  auto go = [&](int kind, bool pair, const HeadArgs& args, int64_t m, int64_t ncols, int splits) {
+    const int64_t tiles = ceil_div(m, pair ? 256 : 128) * ceil_div(ncols, kHeadBN) * splits;
+    const int64_t workers = std::min<int64_t>(tiles, pair ? f.pairs : f.sms);
+    return head_gemm_launch(kind, pair, args, (int)workers * (pair ? 2 : 1), h.st);
   };
   if (!backward) {
-    const int64_t nt = (c.V + kHeadBN - 1) / kHeadBN;
     a.v0 = 0;
     a.vlen = c.V;
-    e = head_gemm_launch(kHeadLse, L.pair, a, grid(L.pair, mt * nt), h.st);
+    e = go(kHeadLse, L.pair_z, a, T, c.V, 1);
     if (e == cudaSuccess)
-      e = launch_head_loss(T, L.K, (int)(2 * nt), L.Tp, temp, distill, r, h.loss, h.lse_out, h.st);
+      e = launch_head_loss(T, L.K, (int)(2 * ceil_div(c.V, kHeadBN)), L.Tp, temp, distill, r, h.loss, h.lse_out, h.st);
     return e == cudaSuccess ? MOE_OK : cuda_bad(w, "launch", e);
   }
-  const int64_t ntd = (c.d + kHeadBN - 1) / kHeadBN;
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += L.piece) {
     const int64_t vlen = std::min<int64_t>(L.piece, c.V - v0);
     a.v0 = ax.v0 = aw.v0 = v0;
     a.vlen = ax.vlen = aw.vlen = vlen;
     ax.add = v0 > 0;
-    e = head_gemm_launch(kHeadDl, L.pair, a, grid(L.pair, mt * ((vlen + kHeadBN - 1) / kHeadBN)), h.st);
-    if (e == cudaSuccess && h.dX) {
-      // a short last piece may have fewer K slices than splits: the empty ones are zeros
-      e = head_gemm_launch(kHeadDX, L.pair, ax, grid(L.pair, mt * ntd * L.nsplit), h.st);
-    }
-    if (e == cudaSuccess && h.dW)
-      e = head_gemm_launch(kHeadDW, pw, aw, grid(pw, (vlen + (pw ? 255 : 127)) / (pw ? 256 : 128) * ntd), h.st);
+    ax.dX = L.nsplit == 1 && v0 + vlen == c.V ? static_cast<__nv_bfloat16*>(h.dX) : nullptr;
+    e = go(kHeadDl, L.pair_z, a, T, vlen, 1);
+    // a short last piece may have fewer K slices than splits: the empty ones add zeros
+    if (e == cudaSuccess && h.dX) e = go(kHeadDX, L.pair_x, ax, T, c.d, L.nsplit);
+    if (e == cudaSuccess && h.dW) e = go(kHeadDW, L.pair_w, aw, vlen, c.d, 1);
   }
-  if (e == cudaSuccess && h.dX) e = launch_head_dx(T, c.d, L.nsplit, L.Tp, temp, r, h.dX, f.sms, h.st);
+  if (e == cudaSuccess && h.dX && L.nsplit > 1)
+    e = launch_head_dx(T, c.d, L.nsplit, L.Tp, temp, r, h.dX, f.sms, h.st);
   return e == cudaSuccess ? MOE_OK : cuda_bad(w, "launch", e);
 }
 

@@ -4,6 +4,7 @@
 // launches them.  Not part of the public ABI.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -30,9 +31,11 @@ struct HeadArgs {
   const int32_t* cnt;        // [T] entries in use, NULL = K
   const float* lse;          // kHeadDl: [T] saved log-sum-exp (of the logits over the temperature)
   const float* dloss;        // kHeadDl: [T] upstream gradient
-  const float* scale;        // kHeadDl: [1] common factor of dloss; kHeadDW: the same, applied to the tile
+  const float* scale;        // [1] common factor of dloss, taken out of D and applied to the sums
   float2* part;              // kHeadLse: [2 * NT, Tp] (max, sum of exp) of 128 columns of one row
   float* zt;                 // kHeadLse: [T, K] logits at the target entries
+  const float* acc;          // kHeadDX: the fp32 sums mapO stores to
+  __nv_bfloat16* dX;         // kHeadDX: [T, d], written instead of the sums (last piece, nsplit = 1); else NULL
   int32_t* status;
   uint64_t timeout_ns;
   int64_t Tp;                // padded rows of the compact buffers
@@ -42,7 +45,7 @@ struct HeadArgs {
   int nsplit;                // kHeadDX: the vocabulary piece is split over this many tiles
   int add;                   // kHeadDX: add into the fp32 sums (0: first piece, overwrite)
   float inv_temp;            // 1 / temperature
-  float out_scale;           // kHeadDW: temperature, multiplied with *scale
+  float out_scale;           // temperature, multiplied with *scale
   int stall;                 // test hook: the producer issues nothing
 };
 
@@ -70,12 +73,14 @@ struct HeadRows {
 
 cudaError_t launch_head_entries(const void* teacher, bool teacher_bf16, const void* ids, bool ids64, int T, int K,
                                 int64_t V, float inv_temp, const HeadRows& r, cudaStream_t st);
+// The list of rows that count and, when some do not, their compact copy of X.
 // labels != NULL: cross entropy (fills r.ids); otherwise r.cnt says which rows count.
-cudaError_t launch_head_scan(const void* labels, bool ids64, const float* dloss, int T, int64_t V, const HeadRows& r,
-                             cudaStream_t st);
-cudaError_t launch_head_gather(const void* X, int T, int d, const HeadRows& r, int num_sms, cudaStream_t st);
+// dX != NULL: rows of tokens that do not count are zeroed.
+cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const void* X, int T, int d, int64_t V,
+                             const HeadRows& r, void* dX, int num_sms, cudaStream_t st);
 cudaError_t launch_head_loss(int T, int K, int np, int64_t Tp, float temperature, bool distill, const HeadRows& r,
                              float* loss, float* lse, cudaStream_t st);
+// dX rows of the tokens that count, from the splits' sums.
 cudaError_t launch_head_dx(int T, int d, int nsplit, int64_t Tp, float out_scale, const HeadRows& r, void* dX,
                            int num_sms, cudaStream_t st);
 

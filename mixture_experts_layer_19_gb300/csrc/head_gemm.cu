@@ -13,19 +13,8 @@ cudaError_t prepare_one() {
 
 template <int KIND, int CG>
 cudaError_t launch_one(const HeadArgs& a, int grid, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kHeadThreads);
-  cfg.dynamicSmemBytes = HeadTraits<KIND, CG>::smem_bytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, head_gemm_kernel<KIND, CG>, a);
+  return launch_pdl(head_gemm_kernel<KIND, CG>, dim3(grid), dim3(kHeadThreads), HeadTraits<KIND, CG>::smem_bytes, st, CG,
+                    a);
 }
 
 template <int CG>

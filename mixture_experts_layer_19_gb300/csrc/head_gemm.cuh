@@ -25,6 +25,7 @@
 // to nearest.  The gradients are rounded to bf16 and do not need it.
 #pragma once
 #include "head.h"
+#include "pdl.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -33,6 +34,7 @@ constexpr int kHBM = 128;                    // rows per CTA
 constexpr int kHBK = 64;                     // K slice (128 bytes of bf16)
 constexpr int kHeadThreads = 320;
 constexpr int kHeadEpiWarps = 8;
+constexpr int kAhead = 2;                    // target entries a row keeps in registers ahead of their columns
 constexpr int kLseChunk = 16;                // K slices per accumulator of kHeadLse (1024)
 
 template <int KIND, int CG>
@@ -44,7 +46,7 @@ struct HeadTraits {
   static constexpr int b_bytes = b_rows * kHBK * 2;           // 32 / 16 KB
   static constexpr int stage_bytes = a_bytes + b_bytes;
   static constexpr int stages = CG == 2 ? 6 : 4;
-  // staging per epilogue warp: 32 x 32 bf16 twice, or 32 x 32 fp32 once
+  // staging per epilogue warp: 32 rows of 128 bytes (64 bf16 or 32 fp32 columns)
   static constexpr int staging = KIND == kHeadLse ? 0 : 4096;
   static constexpr int smem_bytes = stages * stage_bytes + kHeadEpiWarps * staging + 1024 + 256;
 };
@@ -183,16 +185,16 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* m, const vo
                "r"(x), "r"(y), "r"(smem_u32(src))
                : "memory");
 }
-// bf16 block for a 64-byte-swizzled store: 16-byte chunk c of row r at c ^ ((r >> 1) & 3).
-__device__ __forceinline__ void head_stage_bf16(uint8_t* buf, int lane, const float* v) {
-  const int sw = (lane >> 1) & 3;
+// Blocks for 128-byte-swizzled stores: 16-byte chunk c of row r at c ^ (r & 7).
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+// 32 of a row's 64 bf16 columns: the first half or the second.
+__device__ __forceinline__ void head_stage_bf16(uint8_t* buf, int lane, int half, const float* v) {
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ sw) << 4)) =
-        make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                   pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+    *reinterpret_cast<uint4*>(buf + lane * 128 + (((half * 4 + c) ^ (lane & 7)) << 4)) = pack8(v + 8 * c);
 }
-// fp32 block for a 128-byte-swizzled store: chunk c of row r at c ^ (r & 7).
 __device__ __forceinline__ void head_stage_f32(uint8_t* buf, int lane, const uint32_t* v) {
 #pragma unroll
   for (int c = 0; c < 8; ++c)
@@ -259,6 +261,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
   if constexpr (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_release();
   WaitCtl wc{g.status, abort_flag, g.timeout_ns};
 
   const int na = *g.n_active;
@@ -374,7 +378,6 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     const int h = (warp - 2) >> 2;          // column half
     uint8_t* stg = staging_base + (warp - 2) * TR::staging;
     uint32_t acc = 0, aph = 0;
-    uint32_t buf_ctr = 0;
     const float c2 = g.inv_temp * 1.4426950408889634f;   // logits to base-2 exponents
     auto release = [&](uint32_t a) {
       tc_fence_before();
@@ -398,6 +401,25 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         const int cnt = live ? (g.cnt ? g.cnt[tok] : g.K) : 0;
         const int64_t vcol = g.v0 + colh;                         // vocabulary id of the first column
         int e = lower_bound_i32(ids, cnt, vcol);
+        // the row's next entries, read before the products are waited for
+        int64_t nid[kAhead];
+        float np[kAhead];
+        auto entry = [&](int i, int64_t& id, float& p) {
+          const bool in = i < cnt;
+          id = in ? (int64_t)__ldg(ids + i) : INT64_MAX;
+          p = (KIND == kHeadDl && in && g.probs) ? __ldg(g.probs + tok * g.K + i) : 1.0f;
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) entry(e + i, nid[i], np[i]);
+        auto next_entry = [&]() {
+          ++e;
+#pragma unroll
+          for (int i = 0; i + 1 < kAhead; ++i) {
+            nid[i] = nid[i + 1];
+            np[i] = np[i + 1];
+          }
+          entry(e + kAhead - 1, nid[kAhead - 1], np[kAhead - 1]);
+        };
         if constexpr (KIND == kHeadLse) {
           float z[128];
           const int phases = head_phases<KIND>(t.nkb);
@@ -426,16 +448,17 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           if (!ok) break;
           // logits at this row's target entries inside these 128 columns
           while (true) {
-            const int64_t id = e < cnt ? (int64_t)__ldg(ids + e) : INT64_MAX;
-            const bool hit = id < vcol + 128;
+            const bool hit = nid[0] < vcol + 128;
             if (!__any_sync(0xffffffffu, hit)) break;
-            const int col = hit ? (int)(id - vcol) : -1;
+            const int col = hit ? (int)(nid[0] - vcol) : -1;
             float v = 0.0f;
 #pragma unroll
             for (int i = 0; i < 128; ++i)
               if (i == col) v = z[i];
-            if (hit) g.zt[tok * g.K + e] = v;
-            ++e;
+            if (hit) {
+              g.zt[tok * g.K + e] = v;
+              next_entry();
+            }
           }
           const int64_t left = g.vlen - colh;
           if (left < 128) {
@@ -462,7 +485,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           tc_fence_after();
           const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * 128;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 4; ++c) {                           // 32 columns at a time, stored by 64
             uint32_t r[32];
             tmem_ld32(tb + c * 32, r);
             tmem_ld_wait();
@@ -471,29 +494,30 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = ex2_approx(fmaf(__uint_as_float(r[i]), c2, -rl));
             while (true) {
-              const int64_t id = e < cnt ? (int64_t)__ldg(ids + e) : INT64_MAX;
-              const bool hit = id < vcol + c * 32 + 32;
+              const bool hit = nid[0] < vcol + c * 32 + 32;
               if (!__any_sync(0xffffffffu, hit)) break;
-              const int col = hit ? (int)(id - vcol) - c * 32 : -1;
-              const float p = hit ? (g.probs ? __ldg(g.probs + tok * g.K + e) : 1.0f) : 0.0f;
+              const int col = hit ? (int)(nid[0] - vcol) - c * 32 : -1;
+              const float p = np[0];
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (i == col) v[i] -= p;
-              if (hit) ++e;
+              if (hit) next_entry();
             }
             const int64_t left = g.vlen - colh - c * 32;          // columns past the vocabulary are zeros
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = (live && i < left) ? v[i] * gr : 0.0f;
-            uint8_t* buf = stg + (buf_ctr & 1) * 2048;
-            ++buf_ctr;
-            if (lane == 0) bulk_wait_read<1>();
-            __syncwarp();
-            head_stage_bf16(buf, lane, v);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&g.mapO, buf, (int32_t)(colh + c * 32), (int32_t)rowq);
-              bulk_commit();
+            if (!(c & 1)) {
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+            }
+            head_stage_bf16(stg, lane, c & 1, v);
+            if (c & 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&g.mapO, stg, (int32_t)(colh + (c - 1) * 32), (int32_t)rowq);
+                bulk_commit();
+              }
             }
           }
           acc ^= 1;
@@ -506,7 +530,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           tc_fence_after();
         }
         const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * 128;
-        const float sc = KIND == kHeadDW ? *g.scale * g.out_scale : 1.0f;
+        const float sc = *g.scale * g.out_scale;
+        const bool final_dx = KIND == kHeadDX && g.dX != nullptr;
+        const bool live = KIND == kHeadDX && row < na;
+        const int64_t tok = final_dx && live ? g.rowmap[row] : 0;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
@@ -520,31 +547,57 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           }
           const int64_t col = colh + c * 32;
           if constexpr (KIND == kHeadDX) {
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
-            head_stage_f32(stg, lane, r);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && col < g.d && rowq < g.Tp) {
-              const int32_t y = (int32_t)(t.split * g.Tp + rowq);
-              if (g.add) tma_reduce_add_2d(&g.mapO, stg, (int32_t)col, y);
-              else tma_store_2d(&g.mapO, stg, (int32_t)col, y);
-              bulk_commit();
+            if (final_dx) {
+              // last piece, unsplit: add the earlier pieces' sums, round once
+              // and write the token's row
+              if (live) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                  if (col + i >= g.d) break;
+                  float v[8];
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[i + j]);
+                  if (g.add) {
+                    const float4* src = reinterpret_cast<const float4*>(g.acc + row * g.d + col + i);
+                    const float4 p = src[0], q4 = src[1];
+                    v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+                    v[4] += q4.x, v[5] += q4.y, v[6] += q4.z, v[7] += q4.w;
+                  }
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) v[j] *= sc;
+                  *reinterpret_cast<uint4*>(g.dX + tok * g.d + col + i) = pack8(v);
+                }
+              }
+            } else {
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+              head_stage_f32(stg, lane, r);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && col < g.d && rowq < g.Tp) {
+                const int32_t y = (int32_t)(t.split * g.Tp + rowq);
+                if (g.add) tma_reduce_add_2d(&g.mapO, stg, (int32_t)col, y);
+                else tma_store_2d(&g.mapO, stg, (int32_t)col, y);
+                bulk_commit();
+              }
             }
           } else {
-            uint8_t* buf = stg + (buf_ctr & 1) * 2048;
-            ++buf_ctr;
-            if (lane == 0) bulk_wait_read<1>();
-            __syncwarp();
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = has ? __uint_as_float(r[i]) * sc : 0.0f;
-            head_stage_bf16(buf, lane, v);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (col < g.d && rowq < g.vlen) tma_store_2d(&g.mapO, buf, (int32_t)col, (int32_t)(g.v0 + rowq));
-              bulk_commit();
+            if (!(c & 1)) {
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+            }
+            head_stage_bf16(stg, lane, c & 1, v);
+            if (c & 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                const int64_t x = col - 32;
+                if (x < g.d && rowq < g.vlen) tma_store_2d(&g.mapO, stg, (int32_t)x, (int32_t)(g.v0 + rowq));
+                bulk_commit();
+              }
             }
           }
         }

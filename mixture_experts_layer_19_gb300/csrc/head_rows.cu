@@ -5,6 +5,7 @@
 #include <math_constants.h>
 
 #include "head.h"
+#include "pdl.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -26,6 +27,8 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const void* teacher, 
   float* u = reinterpret_cast<float*>(key + Kp2);      // [K]
   __shared__ float red[8];
   __shared__ float s_max, s_sum;
+  pdl_wait();
+  pdl_release();
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
   float m = -CUDART_INF_F;
@@ -121,93 +124,122 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const void* teacher, 
   }
 }
 
-// One block: lists the rows that count, in token order, and (backward) the
-// factor common to their upstream gradients: with one value for all of them
-// (a mean) it is taken out of D before D is rounded to bf16.
-__global__ void __launch_bounds__(1024) head_scan_kernel(const void* labels, int ids64, const float* dloss, int T,
-                                                         int64_t V, HeadRows r) {
-  __shared__ int wsum[32];
-  __shared__ int s_base;
-  __shared__ float smin[32], smax[32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) s_base = 0;
-  float lo = CUDART_INF_F, hi = -CUDART_INF_F;
-  bool odd = false;                                   // an upstream gradient that is not finite
-  __syncthreads();
-  for (int64_t t0 = 0; t0 < T; t0 += 1024) {
-    const int64_t t = t0 + tid;
-    bool on = false;
-    if (t < T) {
-      if (labels) {
-        const int64_t id = load_id(labels, ids64, t);
-        on = id >= 0 && id < V;
-        r.ids[t] = on ? (int32_t)id : -1;
-      } else {
-        on = r.cnt[t] > 0;
-      }
-      if (dloss && on) {
-        const float gv = dloss[t];
-        on = gv != 0.0f;                              // NaN counts
-        if (on) {
-          odd |= !(fabsf(gv) < CUDART_INF_F);
-          lo = fminf(lo, gv);
-          hi = fmaxf(hi, gv);
-        }
-      }
-    }
-    const unsigned b = __ballot_sync(0xffffffffu, on);
-    if (lane == 0) wsum[warp] = __popc(b);
-    __syncthreads();
-    if (warp == 0) {
-      int v = wsum[lane];
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      wsum[lane] = v;
-    }
-    __syncthreads();
-    const int pos = s_base + (warp ? wsum[warp - 1] : 0) + __popc(b & ((1u << lane) - 1u));
-    if (t < T) {
-      r.inv[t] = on ? pos : -1;
-      if (on) r.rowmap[pos] = (int32_t)t;
-    }
-    __syncthreads();
-    if (tid == 0) s_base += wsum[31];
-    __syncthreads();
+__device__ __forceinline__ bool row_counts(const void* labels, bool ids64, const float* dloss, int64_t V,
+                                           const HeadRows& r, int64_t t) {
+  bool on;
+  if (labels) {
+    const int64_t id = load_id(labels, ids64, t);
+    on = id >= 0 && id < V;
+  } else {
+    on = r.cnt[t] > 0;
   }
-  if (tid == 0) r.n_active[0] = s_base;
-  if (!dloss) return;
-  if (odd) lo = -CUDART_INF_F;
+  return on && !(dloss && dloss[t] == 0.0f);          // a NaN gradient counts
+}
+
+// Lists the rows that count, in token order, and copies their rows of X
+// together when some are left out (X is read in place otherwise); zero rows
+// follow up to the next multiple of 256.  Every block walks all T tokens to
+// know how many count before its own and in all -- a few bytes per token from L2,
+// less than a second launch would cost -- and then serves its own range.
+// Block 0 also finds (backward) the factor common to the upstream gradients:
+// with one value for all of them (a mean) it is taken out of D before D is
+// rounded to bf16.
+__global__ void __launch_bounds__(256) head_prep_kernel(const void* labels, int ids64, const float* dloss, int T,
+                                                        int64_t V, const uint4* __restrict__ X, int vecs,
+                                                        HeadRows r, uint4* __restrict__ dX) {
+  __shared__ int s_cnt[8][2];
+  __shared__ float s_lo[8], s_hi[8];
+  __shared__ int s_on[256], s_off[256];                // tokens of the range that count, and that do not
+  pdl_wait();
+  pdl_release();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (T + gridDim.x - 1) / gridDim.x;
+  const int t0 = min(T, (int)blockIdx.x * per), t1 = min(T, t0 + per);
+  int before = 0, total = 0;
+  float lo = CUDART_INF_F, hi = -CUDART_INF_F;
+#pragma unroll 4
+  for (int t = tid; t < T; t += 256) {
+    const bool on = row_counts(labels, ids64, dloss, V, r, t);
+    total += on;
+    before += on && t < t0;
+    if (dloss && on && blockIdx.x == 0) {
+      const float gv = dloss[t];
+      if (!(fabsf(gv) < CUDART_INF_F)) lo = -CUDART_INF_F;    // not finite: no common factor
+      lo = fminf(lo, gv);
+      hi = fmaxf(hi, gv);
+    }
+  }
   for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   if (lane == 0) {
-    smin[warp] = lo;
-    smax[warp] = hi;
+    s_cnt[warp][0] = before;
+    s_cnt[warp][1] = total;
+    s_lo[warp] = lo;
+    s_hi[warp] = hi;
   }
   __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < 32; ++i) {
-      lo = fminf(lo, smin[i]);
-      hi = fmaxf(hi, smax[i]);
-    }
-    *r.scale = lo == hi ? lo : 1.0f;
+  before = total = 0;
+  for (int i = 0; i < 8; ++i) {
+    before += s_cnt[i][0];
+    total += s_cnt[i][1];
   }
-}
-
-// Compact copy of the rows that count, zero rows up to the next multiple of
-// 256.  Nothing to do when every row counts (X is then read in place).
-__global__ void __launch_bounds__(256) head_gather_kernel(const uint4* __restrict__ X, int T, int vecs, HeadRows r) {
-  const int na = *r.n_active;
-  if (na == T) return;
-  const int rows = (na + kHeadRowPad - 1) / kHeadRowPad * kHeadRowPad;
+  if (blockIdx.x == 0 && tid == 0) {
+    for (int i = 1; i < 8; ++i) {
+      lo = fminf(lo, s_lo[i]);
+      hi = fmaxf(hi, s_hi[i]);
+    }
+    r.n_active[0] = total;
+    *r.scale = lo == hi && fabsf(lo) < CUDART_INF_F ? lo : 1.0f;
+  }
+  const bool copy = total != T;
   uint4* out = reinterpret_cast<uint4*>(r.Xc);
-  for (int i = blockIdx.x; i < rows; i += gridDim.x) {
-    const int64_t src = i < na ? r.rowmap[i] : -1;
-    for (int c = threadIdx.x; c < vecs; c += blockDim.x)
-      out[(int64_t)i * vecs + c] = src >= 0 ? X[src * vecs + c] : make_uint4(0, 0, 0, 0);
+  for (int base = t0; base < t1; base += 256) {
+    const int t = base + tid;
+    const bool on = t < t1 && row_counts(labels, ids64, dloss, V, r, t);
+    const unsigned b = __ballot_sync(0xffffffffu, on);
+    __syncthreads();                                   // the lists are free again
+    if (lane == 0) s_cnt[warp][0] = __popc(b);
+    __syncthreads();
+    int at = __popc(b & ((1u << lane) - 1u)), n = 0;
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) at += s_cnt[i][0];
+      n += s_cnt[i][0];
+    }
+    if (t < t1) {
+      r.inv[t] = on ? before + at : -1;
+      if (labels) r.ids[t] = on ? (int32_t)load_id(labels, ids64, t) : -1;
+    }
+    const int rows = min(256, t1 - base);
+    if (on) {
+      r.rowmap[before + at] = t;
+      s_on[at] = t;
+    } else if (t < t1) {
+      s_off[tid - at] = t;
+    }
+    __syncthreads();
+    if (copy) {
+      const int64_t all = (int64_t)n * vecs;
+#pragma unroll 4
+      for (int64_t i = tid; i < all; i += 256) {
+        const int row = (int)(i / vecs), c = (int)(i - (int64_t)row * vecs);
+        out[(int64_t)(before + row) * vecs + c] = X[(int64_t)s_on[row] * vecs + c];
+      }
+      if (dX)
+        for (int64_t i = tid; i < (int64_t)(rows - n) * vecs; i += 256) {
+          const int row = (int)(i / vecs), c = (int)(i - (int64_t)row * vecs);
+          dX[(int64_t)s_off[row] * vecs + c] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    before += n;
+  }
+  if (copy) {
+    const int pad = (total + kHeadRowPad - 1) / kHeadRowPad * kHeadRowPad;
+    for (int i = total + (int)blockIdx.x; i < pad; i += gridDim.x)
+      for (int c = tid; c < vecs; c += 256) out[(int64_t)i * vecs + c] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -218,6 +250,8 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const uint4* __restric
 __global__ void __launch_bounds__(1024) head_loss_kernel(int T, int K, int np, int64_t Tp, float temperature,
                                                          int distill, HeadRows r, float* loss, float* lse) {
   __shared__ float sm[32][33], ss[32][33];
+  pdl_wait();
+  pdl_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = blockIdx.x * 32;
   {
@@ -276,30 +310,28 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(int T, int K, int np, i
   }
 }
 
-// dX[t] = factor * (sum over the splits, in order) for the rows that count, 0 elsewhere.
-__global__ void __launch_bounds__(256) head_dx_kernel(int T, int d, int nsplit, int64_t Tp, float out_scale, HeadRows r,
+// dX of each token that counts = factor * (sum over the splits, in order).
+__global__ void __launch_bounds__(256) head_dx_kernel(int d, int nsplit, int64_t Tp, float out_scale, HeadRows r,
                                                       uint2* __restrict__ dX) {
+  pdl_wait();
+  pdl_release();
   const int vecs = d / 4;
   const float sc = *r.scale * out_scale;
   const float4* acc = reinterpret_cast<const float4*>(r.acc);
-  const int64_t n = (int64_t)T * vecs;
+  const int64_t n = (int64_t)*r.n_active * vecs;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t t = i / vecs;
-    const int c = (int)(i - t * vecs);
-    const int row = r.inv[t];
-    uint2 o = make_uint2(0, 0);
-    if (row >= 0) {
-      float4 a = acc[(int64_t)row * vecs + c];
-      for (int s = 1; s < nsplit; ++s) {
-        const float4 b = acc[(s * Tp + row) * vecs + c];
-        a.x += b.x;
-        a.y += b.y;
-        a.z += b.z;
-        a.w += b.w;
-      }
-      o = make_uint2(pack_bf16(a.x * sc, a.y * sc), pack_bf16(a.z * sc, a.w * sc));
+    const int64_t row = i / vecs;
+    const int c = (int)(i - row * vecs);
+    float4 a = acc[i];
+#pragma unroll 4
+    for (int s = 1; s < nsplit; ++s) {
+      const float4 b = acc[(s * Tp + row) * vecs + c];
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
     }
-    dX[i] = o;
+    dX[(int64_t)r.rowmap[row] * vecs + c] = make_uint2(pack_bf16(a.x * sc, a.y * sc), pack_bf16(a.z * sc, a.w * sc));
   }
 }
 
@@ -311,35 +343,29 @@ cudaError_t launch_head_entries(const void* teacher, bool teacher_bf16, const vo
   while (kp < K) kp <<= 1;
   int threads = 32;
   while (threads < kp / 2 && threads < 256) threads <<= 1;
-  head_entries_kernel<<<T, threads, kp * 8 + K * 4, st>>>(teacher, teacher_bf16, ids, ids64, K, kp, V, inv_temp, r);
-  return cudaGetLastError();
+  return launch_pdl(head_entries_kernel, dim3(T), dim3(threads), kp * 8 + K * 4, st, 1, teacher, (int)teacher_bf16, ids,
+                    (int)ids64, K, kp, V, inv_temp, r);
 }
 
-cudaError_t launch_head_scan(const void* labels, bool ids64, const float* dloss, int T, int64_t V, const HeadRows& r,
-                             cudaStream_t st) {
-  head_scan_kernel<<<1, 1024, 0, st>>>(labels, ids64, dloss, T, V, r);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_head_gather(const void* X, int T, int d, const HeadRows& r, int num_sms, cudaStream_t st) {
-  const int rows = (T + kHeadRowPad - 1) / kHeadRowPad * kHeadRowPad;
-  head_gather_kernel<<<rows < 8 * num_sms ? rows : 8 * num_sms, 256, 0, st>>>(reinterpret_cast<const uint4*>(X), T,
-                                                                             d / 8, r);
-  return cudaGetLastError();
+cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const void* X, int T, int d, int64_t V,
+                             const HeadRows& r, void* dX, int num_sms, cudaStream_t st) {
+  // few tokens per block, so that a block's copy is short, up to one wave of blocks
+  const int blocks = (T + 3) / 4 < 8 * num_sms ? (T + 3) / 4 : 8 * num_sms;
+  return launch_pdl(head_prep_kernel, dim3(blocks), dim3(256), 0, st, 1, labels, (int)ids64, dloss, T, V,
+                    reinterpret_cast<const uint4*>(X), d / 8, r, reinterpret_cast<uint4*>(dX));
 }
 
 cudaError_t launch_head_loss(int T, int K, int np, int64_t Tp, float temperature, bool distill, const HeadRows& r,
                              float* loss, float* lse, cudaStream_t st) {
-  head_loss_kernel<<<(T + 31) / 32, 1024, 0, st>>>(T, K, np, Tp, temperature, distill, r, loss, lse);
-  return cudaGetLastError();
+  return launch_pdl(head_loss_kernel, dim3((T + 31) / 32), dim3(1024), 0, st, 1, T, K, np, Tp, temperature, (int)distill,
+                    r, loss, lse);
 }
 
 cudaError_t launch_head_dx(int T, int d, int nsplit, int64_t Tp, float out_scale, const HeadRows& r, void* dX,
                            int num_sms, cudaStream_t st) {
   const int64_t n = ((int64_t)T * (d / 4) + 255) / 256;
-  head_dx_kernel<<<(int)(n < 8 * num_sms ? n : 8 * num_sms), 256, 0, st>>>(T, d, nsplit, Tp, out_scale, r,
-                                                                          reinterpret_cast<uint2*>(dX));
-  return cudaGetLastError();
+  return launch_pdl(head_dx_kernel, dim3((unsigned)(n < 8 * num_sms ? n : 8 * num_sms)), dim3(256), 0, st, 1, d, nsplit,
+                    Tp, out_scale, r, reinterpret_cast<uint2*>(dX));
 }
 
 }  // namespace moe

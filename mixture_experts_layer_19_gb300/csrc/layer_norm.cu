@@ -9,7 +9,7 @@
 //                        16-byte registers vectors per lane, weights in shared
 //                        memory; with one warp there is no barrier at all
 //   few rows, odd widths one block per row
-//   backward             one block per row pair; each thread keeps its columns'
+//   backward             one block per row; each thread keeps its columns'
 //                        sums of dw and db in registers over all its rows and
 //                        prefetches later rows into its own shared memory
 //   rows past 8192 elements are read again instead of kept
@@ -25,6 +25,7 @@
 
 #include "kernels.h"
 #include "moe.h"
+#include "pdl.cuh"
 
 namespace moe {
 namespace {
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) ln_fwd_rows_kernel(const ui
       const int c = tid + j * nt;
       v[j] = c < vecs ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
     }
-    f2 s2 = 0, t2 = 0;
+    f2 s2 = f2_make(0, 0), t2 = s2;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) ln_fwd_rows_kernel(const ui
     float2 s = f2_get(f2_add(s2, t2));
     const float m = row_sum(s.x + s.y, red[0]) * inv_d;
     const f2 mm = f2_make(-m, -m);
-    s2 = t2 = 0;
+    s2 = t2 = f2_make(0, 0);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (tid + j * nt < vecs) {
@@ -333,154 +334,143 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
                : "memory");
 }
-// Sums of four values over the block, the same on every thread.
-__device__ __forceinline__ void block_sum4(float (&s)[4], float4* red, int nw) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // lane l of a quad ends with value l: 2 + 1 exchanges instead of 4 sums of 2 steps
-  const bool b0 = lane & 1, b1 = lane & 2;
-  float a = b0 ? s[1] : s[0], c = b0 ? s[3] : s[2];
-  a += __shfl_xor_sync(0xffffffffu, b0 ? s[0] : s[1], 1);
-  c += __shfl_xor_sync(0xffffffffu, b0 ? s[2] : s[3], 1);
-  float e = b1 ? c : a;
-  e += __shfl_xor_sync(0xffffffffu, b1 ? a : c, 2);
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
-  if (lane < 4) reinterpret_cast<float*>(red + warp)[lane] = e;
-  __syncthreads();
-  f2 p = 0, q = 0;
-  for (int w = 0; w < nw; ++w) {
-    const float4 v = red[w];
-    p = f2_add(p, f2_make(v.x, v.y));
-    q = f2_add(q, f2_make(v.z, v.w));
-  }
-  const float2 x = f2_get(p), y = f2_get(q);
-  s[0] = x.x;
-  s[1] = x.y;
-  s[2] = y.x;
-  s[3] = y.y;
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
 }
 
-// Two rows per step, `depth` (even) rows prefetched with cp.async.  A thread
-// reads from shared memory only what it copied there itself, so the copies
-// need no barrier; the one per step is the reduction's.
-template <class XT, int VPT>
+// DEPTH rows are prefetched with cp.async.  A thread reads from shared memory
+// only what it copied there itself, so the copies need no barrier.  The two
+// halves of a row's work -- its sums, then its dx -- are a step apart: a step
+// adds up row k, then finishes row k - 1 from registers while the other warps'
+// sums of row k arrive, and ends with the one barrier that row needs.  What
+// bounds it is issuing: about 11 fp32 operations and the conversions per
+// element, so everything per row that is not per element is kept out of the loop.
+template <class XT, int VPT, int DEPTH>
 __global__ void __launch_bounds__(kMaxThreads, 1) ln_bwd_rows_kernel(
     const uint4* __restrict__ dy, const uint4* __restrict__ x, const void* w, bool w_f32,
-    const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows, int d, int depth,
+    const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows, int d,
     uint4* __restrict__ dx, float* __restrict__ part_w, float* __restrict__ part_b) {
   using P = Pairs<XT>;
-  extern __shared__ uint4 ring[];                        // [depth][2][vecs]
-  __shared__ float4 red[2][16];
-  const int vecs = d / (2 * P::n), nw = blockDim.x >> 5, tid = threadIdx.x;
+  extern __shared__ uint4 ring[];                        // [DEPTH][2][VPT * threads]
+  __shared__ float2 red[2][32];                          // warps the block does not have stay 0
+  __shared__ float2 stats[DEPTH][32];                    // (mean, rstd) of a row, copied by each warp for itself
+  pdl_release();
+  const int vecs = d / (2 * P::n), tid = threadIdx.x, nt = blockDim.x;
+  if (tid < 32) red[0][tid] = red[1][tid] = make_float2(0.0f, 0.0f);
+  __syncthreads();
+  const int warp = tid >> 5, lane = tid & 31;
   const float inv_d = 1.0f / (float)d;
   f2 wr[VPT][P::n], aw[VPT][P::n], ab[VPT][P::n];
+  bool in[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int c = tid + j * blockDim.x;
+    const int c = tid + j * nt;
+    in[j] = c < vecs;
 #pragma unroll
     for (int p = 0; p < P::n; ++p) {
       const int e = c * 2 * P::n + 2 * p;
-      wr[j][p] = c < vecs ? f2_make(weight_at(w, w_f32, e), weight_at(w, w_f32, e + 1)) : 0;
-      aw[j][p] = ab[j][p] = 0;
+      wr[j][p] = in[j] ? f2_make(weight_at(w, w_f32, e), weight_at(w, w_f32, e + 1)) : f2_make(0, 0);
+      aw[j][p] = ab[j][p] = f2_make(0, 0);
     }
+    // slots of columns past the row stay zero: they add nothing
+    if (!in[j])
+      for (int k = 0; k < DEPTH; ++k)
+        ring[((2 * k) * VPT + j) * nt + tid] = ring[((2 * k + 1) * VPT + j) * nt + tid] = make_uint4(0, 0, 0, 0);
   }
-  const int64_t mine = (rows - blockIdx.x + gridDim.x - 1) / gridDim.x;    // rows blockIdx.x + k * gridDim.x
-  auto fetch = [&](int64_t k, int slot) {
-    if (k < mine) {
-      const int64_t base = ((int64_t)blockIdx.x + k * gridDim.x) * vecs;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int c = tid + j * blockDim.x;
-        if (c < vecs) {
-          cp_async16(ring + (2 * slot) * vecs + c, x + base + c);
-          cp_async16(ring + (2 * slot + 1) * vecs + c, dy + base + c);
-        }
-      }
-    }
-  };
-  for (int k = 0; k < depth; k += 2) {
-    fetch(k, k);
-    fetch(k + 1, k + 1);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  int slot = 0, flip = 0;
-  for (int64_t k = 0; k < mine; k += 2) {
-    float m[2], rs[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t r = (int64_t)blockIdx.x + (k + u) * gridDim.x;
-      m[u] = k + u < mine ? __ldg(mean + r) : 0.0f;
-      rs[u] = k + u < mine ? __ldg(rstd + r) : 0.0f;
-    }
-    // the pair of rows copied longest ago has landed
-    if (depth >= 8) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (depth == 6) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (depth == 4) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
-    uint4 vx[2][VPT], vg[2][VPT];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int c = tid + j * blockDim.x;
-        const bool in = c < vecs && k + u < mine;
-        vx[u][j] = in ? ring[(2 * (slot + u)) * vecs + c] : make_uint4(0, 0, 0, 0);
-        vg[u][j] = in ? ring[(2 * (slot + u) + 1) * vecs + c] : make_uint4(0, 0, 0, 0);
-      }
-    fetch(k + depth, slot);
-    fetch(k + depth + 1, slot + 1);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    slot = slot + 2 == depth ? 0 : slot + 2;
-    float s[4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const f2 rr = f2_make(rs[u], rs[u]), mm = f2_make(-m[u], -m[u]);
-      f2 s0 = 0, s1 = 0;
+  const int mine = (int)((rows - blockIdx.x + gridDim.x - 1) / gridDim.x);    // rows blockIdx.x + k * gridDim.x
+  const int64_t stride = (int64_t)gridDim.x * vecs;
+  const uint4* fx = x + (int64_t)blockIdx.x * vecs + tid;
+  const uint4* fg = dy + (int64_t)blockIdx.x * vecs + tid;
+  uint4* out = dx + (int64_t)blockIdx.x * vecs + tid;
+  const float* fs = (lane == 0 ? mean : rstd) + blockIdx.x;
+  int to_fetch = mine;
+  auto fetch = [&](uint4* slot, float2* st) {
+    if (to_fetch > 0) {
+      if (lane < 2) cp_async4(reinterpret_cast<float*>(st) + lane, fs);
+      fs += gridDim.x;
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int p = 0; p < P::n; ++p) {
-          // columns past the row have dy = 0 and add nothing
-          const f2 n = f2_mul(f2_add(P::get(vx[u][j], p), mm), rr), g = P::get(vg[u][j], p);
-          const f2 gw = f2_mul(g, wr[j][p]);
-          s0 = f2_add(s0, gw);
-          s1 = f2_fma(gw, n, s1);
-          aw[j][p] = f2_fma(g, n, aw[j][p]);
-          ab[j][p] = f2_add(ab[j][p], g);
+        if (in[j]) {
+          cp_async16(slot + j * nt, fx + j * nt);
+          cp_async16(slot + (VPT + j) * nt, fg + j * nt);
         }
-      const float2 a = f2_get(s0), c = f2_get(s1);
-      s[2 * u] = a.x + a.y;
-      s[2 * u + 1] = c.x + c.y;
+      fx += stride;
+      fg += stride;
+      --to_fetch;
     }
-    if (!dx) continue;
-    keep_packed<VPT>(vx[0]);
-    keep_packed<VPT>(vx[1]);
-    keep_packed<VPT>(vg[0]);
-    keep_packed<VPT>(vg[1]);
-    block_sum4(s, red[flip], nw);
-    flip ^= 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  uint4* const first = ring + tid;
+  uint4* const past = first + DEPTH * 2 * VPT * nt;
+  for (int k = 0; k < DEPTH; ++k) fetch(first + k * 2 * VPT * nt, &stats[k][warp]);
+  uint4* slot = first;
+  float2* st = &stats[0][warp];
+  f2 px[VPT][P::n], pg[VPT][P::n];                       // row k - 1: x - mean, rstd g w
+  float rs0 = 0.0f;                                      // rstd of row k - 1
+#pragma unroll 2
+  for (int k = 0; k <= mine; ++k) {
+    const float* row_red = reinterpret_cast<const float*>(red[(k + 1) & 1]);
+    // totals of row k - 1: lane l adds value (l & 1) of the warps l / 2 and l / 2 + 16
+    float tot = 0.0f;
+    if (dx && k > 0) {
+      tot = row_red[lane] + row_red[lane + 32];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (k + u >= mine) break;
-      const f2 rr = f2_make(rs[u], rs[u]), mm = f2_make(-m[u], -m[u]);
-      const float c1 = -s[2 * u] * inv_d, c2 = -s[2 * u + 1] * inv_d;
+      for (int o = 2; o < 32; o <<= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+      // with s0 = rstd sum(g w), s1 = rstd sum(g w (x - mean)):
+      // dx = rstd g w - s0 / d - (x - mean) rstd^2 s1 / d
+      const float c1 = -__shfl_sync(0xffffffffu, tot, 0) * inv_d;
+      const float c2 = -__shfl_sync(0xffffffffu, tot, 1) * inv_d * rs0 * rs0;
       const f2 k1 = f2_make(c1, c1), k2 = f2_make(c2, c2);
-      const int64_t base = ((int64_t)blockIdx.x + (k + u) * gridDim.x) * vecs;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int c = tid + j * blockDim.x;
-        if (c < vecs) {
-          uint4 o;
+        uint4 o;
 #pragma unroll
-          for (int p = 0; p < P::n; ++p) {
-            const f2 n = f2_mul(f2_add(P::get(vx[u][j], p), mm), rr);
-            const f2 t = f2_fma(P::get(vg[u][j], p), wr[j][p], k1);
-            P::set(o, p, f2_mul(rr, f2_fma(n, k2, t)));
-          }
-          __stcs(dx + base + c, o);
+        for (int p = 0; p < P::n; ++p) P::set(o, p, f2_fma(px[j][p], k2, f2_add(pg[j][p], k1)));
+        if (in[j]) __stcs(out + j * nt, o);
+      }
+      out += stride;
+    }
+    if (k < mine) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+      __syncwarp();
+      const float m = st->x, rs = st->y;
+      __syncwarp();                                      // before lanes 0 and 1 copy over it
+      const f2 rr = f2_make(rs, rs), mm = f2_make(-m, -m);
+      f2 s0 = f2_make(0, 0), s1 = s0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const uint4 vx = slot[j * nt], vg = slot[(VPT + j) * nt];
+#pragma unroll
+        for (int p = 0; p < P::n; ++p) {
+          const f2 xm = f2_add(P::get(vx, p), mm), g = P::get(vg, p);
+          const f2 gr = f2_mul(g, rr), gw = f2_mul(gr, wr[j][p]);
+          s0 = f2_add(s0, gw);
+          s1 = f2_fma(gw, xm, s1);
+          aw[j][p] = f2_fma(gr, xm, aw[j][p]);
+          ab[j][p] = f2_add(ab[j][p], g);
+          px[j][p] = xm;
+          pg[j][p] = gw;
         }
       }
+      fetch(slot, st);
+      slot += 2 * VPT * nt;
+      st += 32;
+      if (slot == past) {
+        slot = first;
+        st = &stats[0][warp];
+      }
+      rs0 = rs;
+      const float2 a = f2_get(s0), c = f2_get(s1);
+      const float t0 = a.x + a.y, t1 = c.x + c.y;
+      // even lanes end with the sum of t0, odd lanes with that of t1
+      float e = (lane & 1) ? t1 : t0;
+      e += __shfl_xor_sync(0xffffffffu, (lane & 1) ? t0 : t1, 1);
+#pragma unroll
+      for (int o = 2; o < 32; o <<= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+      if (lane < 2) reinterpret_cast<float*>(&red[k & 1][warp])[lane] = e;
     }
+    __syncthreads();
   }
   if (!part_w) return;
   const int64_t base = (int64_t)blockIdx.x * d;
@@ -599,6 +589,7 @@ __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__
                                                        const float* __restrict__ part_b, int G, int d,
                                                        WT* __restrict__ dw, WT* __restrict__ db) {
   __shared__ float sw[32][33], sb[32][33];
+  pdl_wait();
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.0f, b = 0.0f;
@@ -718,6 +709,17 @@ int current_sms() {
   return std::max(1, sms);
 }
 
+// The backward on 16-byte accesses: 16 elements per thread, or one access
+// where that would leave a block with less than two warps.
+Shape bwd_shape(int64_t d, int esize) {
+  Shape s = shape_of(d, esize);
+  if (s.vw == 1 || !s.reg) return s;
+  const int64_t vecs = d / s.vw;
+  s.vpt = vecs < 128 ? 1 : kMaxElems / s.vw;
+  s.threads = (int)(((vecs + s.vpt - 1) / s.vpt + 31) / 32 * 32);
+  return s;
+}
+
 // Blocks of the persistent kernels; the backward's number of column partials.
 int64_t fwd_blocks(int64_t rows, const Shape& s, int sms) {
   return std::min<int64_t>(rows, (int64_t)sms * std::max(1, std::min(16, 2048 / s.threads)));
@@ -770,18 +772,28 @@ cudaError_t fwd_rows_go(const void* x, const void* w, const void* b, bool w_f32,
   return cudaGetLastError();
 }
 
+template <class XT, int VPT, int DEPTH>
+cudaError_t bwd_depth_go(const void* dy, const void* x, const void* w, bool w_f32, const float* mean, const float* rstd,
+                         int64_t rows, int d, void* dx, float* pw, float* pb, const Shape& s, int64_t blocks,
+                         cudaStream_t st) {
+  const int smem = DEPTH * 2 * VPT * s.threads * 16;
+  auto kernel = ln_bwd_rows_kernel<XT, VPT, DEPTH>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)blocks, s.threads, smem, st>>>((const uint4*)dy, (const uint4*)x, w, w_f32, mean, rstd, rows, d,
+                                                   (uint4*)dx, pw, pb);
+  return cudaGetLastError();
+}
+// As many rows in flight as shared memory has room for, up to 7.
 template <class XT, int VPT>
 cudaError_t bwd_rows_go(const void* dy, const void* x, const void* w, bool w_f32, const float* mean, const float* rstd,
                         int64_t rows, int d, void* dx, float* pw, float* pb, const Shape& s, int64_t blocks,
                         cudaStream_t st) {
-  const int pair = 2 * 2 * d * (int)sizeof(XT);          // two rows of x and dy
-  const int depth = 2 * std::max(1, std::min(4, (200 << 10) / pair / std::max(1, std::min(8, 512 / s.threads))));
-  auto kernel = ln_bwd_rows_kernel<XT, VPT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, depth / 2 * pair);
-  if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)blocks, s.threads, depth / 2 * pair, st>>>((const uint4*)dy, (const uint4*)x, w, w_f32, mean, rstd,
-                                                               rows, d, depth, (uint4*)dx, pw, pb);
-  return cudaGetLastError();
+  const int per_sm = std::max(1, std::min(8, 512 / s.threads));
+  const int fit = (220 << 10) / (2 * VPT * s.threads * 16) / per_sm;
+  if (fit >= 7) return bwd_depth_go<XT, VPT, 7>(dy, x, w, w_f32, mean, rstd, rows, d, dx, pw, pb, s, blocks, st);
+  if (fit >= 5) return bwd_depth_go<XT, VPT, 5>(dy, x, w, w_f32, mean, rstd, rows, d, dx, pw, pb, s, blocks, st);
+  return bwd_depth_go<XT, VPT, 3>(dy, x, w, w_f32, mean, rstd, rows, d, dx, pw, pb, s, blocks, st);
 }
 
 // Calls GO<XT, WT, VW, VPT>(args...) for the shape's access width and count.
@@ -828,10 +840,9 @@ cudaError_t bwd_rows(const void* dy, const void* x, const void* w, const float* 
                      int64_t d, void* dx, float* pw, float* pb, const Shape& s, int64_t blocks, cudaStream_t st) {
   if (s.reg && s.vw > 1) {
     const bool wf = sizeof(WT) == 4;
-    if (s.vpt == 1) return bwd_rows_go<XT, 1>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
-    if (s.vpt == 2) return bwd_rows_go<XT, 2>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
-    return bwd_rows_go<XT, kMaxElems * (int)sizeof(XT) / 16>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s,
-                                                            blocks, st);
+    constexpr int kWide = kMaxElems * (int)sizeof(XT) / 16;
+    return s.vpt == 1 ? bwd_rows_go<XT, 1>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st)
+                      : bwd_rows_go<XT, kWide>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
   }
   if (s.reg) LN_SCALAR(bwd_go, dy, x, w, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
   cudaError_t e = cudaSuccess;
@@ -849,22 +860,22 @@ cudaError_t bwd_rows(const void* dy, const void* x, const void* w, const float* 
 }
 
 int64_t partials_of(int64_t rows, int64_t d, int esize, int sms) {
-  const Shape s = shape_of(d, esize);
+  const Shape s = bwd_shape(d, esize);
   return s.reg ? bwd_blocks(rows, s.threads, sms) : long_slices(rows);
 }
 
 template <class XT, class WT>
 cudaError_t bwd_types(const void* dy, const void* x, const void* w, const float* mean, const float* rstd, int64_t rows,
                       int64_t d, void* dx, void* dw, void* db, float* ws, cudaStream_t st) {
-  const Shape s = shape_of(d, sizeof(XT));
+  const Shape s = bwd_shape(d, sizeof(XT));
   const int64_t G = partials_of(rows, d, sizeof(XT), current_sms());
   const bool sums = dw || db;
   float* pw = sums ? ws : nullptr;
   float* pb = sums ? ws + G * d : nullptr;
   cudaError_t e = bwd_rows<XT, WT>(dy, x, w, mean, rstd, rows, d, dx, pw, pb, s, G, st);
   if (e != cudaSuccess || !sums) return e;
-  ln_cols_kernel<WT><<<(unsigned)((d + 31) / 32), 1024, 0, st>>>(pw, pb, (int)G, (int)d, (WT*)dw, (WT*)db);
-  return cudaGetLastError();
+  return launch_pdl(ln_cols_kernel<WT>, dim3((unsigned)((d + 31) / 32)), dim3(1024), 0, st, 1, pw, pb, (int)G, (int)d,
+                    (WT*)dw, (WT*)db);
 }
 
 moe_status_t bad(const char* where, const char* what) {

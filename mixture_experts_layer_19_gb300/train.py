@@ -18,8 +18,8 @@ an argument before anything is enqueued.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -28,6 +28,9 @@ from . import moe
 from .moe import MOE_DEBUG_STALL_TEST, moe_head_config_t  # noqa: F401  (MOE_DEBUG_STALL_TEST: tests)
 
 _BF16, _F32 = torch.bfloat16, torch.float32
+_I32, _I64 = torch.int32, torch.int64
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _check(status: int, where: str) -> None:
@@ -35,55 +38,57 @@ def _check(status: int, where: str) -> None:
         raise moe.MoEError(status, where)
 
 
-def _need(ok: bool, message: str) -> None:
-    if not ok:
-        raise ValueError(message)
+def _device_of(t: torch.Tensor, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    return index
 
 
-def _cuda(device: torch.device, **tensors) -> None:
-    """Every given tensor is a contiguous, 16-byte aligned tensor on `device`."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        _need(t.is_cuda and t.device == device, f"{name}: expected a tensor on {device}, got {t.device}")
-        _need(t.is_contiguous(), f"{name}: must be contiguous")
-        _need(t.data_ptr() % 16 == 0, f"{name}: must be 16-byte aligned")
+def _ptr(t: torch.Tensor, name: str, index: int, align: int = 16) -> int:
+    """The address of a contiguous tensor on GPU `index`, aligned to `align` bytes."""
+    p = t.data_ptr()
+    if p % align or t.get_device() != index or not t.is_contiguous():
+        if t.get_device() != index:
+            raise ValueError(f"{name}: expected a tensor on cuda:{index}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        raise ValueError(f"{name}: must be {align}-byte aligned")
+    return p
 
 
-def _scope(device: torch.device, stream: Optional[torch.cuda.Stream]):
-    """The device and stream a call runs on: outputs and workspace are allocated there too."""
+def _elsewhere(index: int, stream: Optional[torch.cuda.Stream]):
+    """The context a call has to run in when that is not the current one: the given stream, or the
+    tensors' GPU.  Outputs and workspace are then allocated there too."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    if device.index is not None and device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    if index != torch.cuda.current_device():
+        return torch.cuda.device(index)
+    return None
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _workspace(nbytes: int, device: torch.device) -> torch.Tensor:
-    return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 _status = {}
 
 
-def _status_word(device: torch.device) -> torch.Tensor:
+def _status_word(index: int) -> torch.Tensor:
     """One device word per GPU that receives a kernel's timeout code."""
-    s = _status.get(device)
+    s = _status.get(index)
     if s is None:
-        s = _status[device] = torch.zeros((1,), dtype=torch.int32, device=device)
-        torch.cuda.current_stream(device).synchronize()   # zeroed before any stream's kernels use it
+        s = torch.zeros((1,), dtype=_I32, device=torch.device("cuda", index))
+        torch.cuda.current_stream(index).synchronize()   # zeroed before any stream's kernels use it
+        _status[index] = s
     return s
 
 
 def device_status(device=0) -> int:
     """Waits for the GPU, returns the status the loss head's kernels left there (0, or
     moe.MOE_ERR_TIMEOUT after a device-side wait expired) and clears it."""
-    dev = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
-    s = _status_word(torch.device("cuda", dev.index if dev.index is not None else torch.cuda.current_device()))
+    index = device if isinstance(device, int) else torch.device(device).index
+    s = _status_word(torch.cuda.current_device() if index is None else index)
     torch.cuda.synchronize(s.device)
     code = int(s.item())
     if code:
@@ -93,15 +98,20 @@ def device_status(device=0) -> int:
 
 
 # ------------------------------------------------------------------ layer norm
-def _ln_args(x, weight, other=()):
-    _need(x is not None and x.dim() >= 1, "x: expected at least one dimension")
-    _need(x.dtype in (_BF16, _F32), f"x: dtype {x.dtype}, expected torch.bfloat16 or torch.float32")
-    d = x.shape[-1]
-    _need(d >= 1, "x: the last dimension must not be empty")
-    _need(weight is not None, "weight is required")
-    _need(weight.dtype in (_BF16, _F32), f"weight: dtype {weight.dtype}, expected torch.bfloat16 or torch.float32")
-    _need(tuple(weight.shape) == (d,), f"weight: shape {tuple(weight.shape)}, expected {(d,)}")
-    return x.numel() // d, d
+def _ln_args(x, weight):
+    if x is None or weight is None:
+        raise ValueError("x and weight are required")
+    if x.dtype is not _BF16 and x.dtype is not _F32:
+        raise ValueError(f"x: dtype {x.dtype}, expected torch.bfloat16 or torch.float32")
+    if weight.dtype is not _BF16 and weight.dtype is not _F32:
+        raise ValueError(f"weight: dtype {weight.dtype}, expected torch.bfloat16 or torch.float32")
+    shape = x.shape
+    if not shape or not shape[-1]:
+        raise ValueError(f"x: shape {tuple(shape)}, expected a last dimension that is not empty")
+    d = shape[-1]
+    if weight.shape != (d,):
+        raise ValueError(f"weight: shape {tuple(weight.shape)}, expected {(d,)}")
+    return shape, x.numel() // d, d
 
 
 def layer_norm_forward(x, weight, bias=None, eps: float = 1e-5, stream=None
@@ -110,47 +120,58 @@ def layer_norm_forward(x, weight, bias=None, eps: float = 1e-5, stream=None
 
     x: bf16 or fp32, y likewise; weight and bias: both bf16 or both fp32; mean
     and rstd: fp32 of x's leading shape."""
-    rows, d = _ln_args(x, weight)
+    shape, rows, d = _ln_args(x, weight)
+    index = _device_of(x, "x")
+    xp, wp, bp = _ptr(x, "x", index), _ptr(weight, "weight", index), None
     if bias is not None:
-        _need(bias.dtype == weight.dtype and tuple(bias.shape) == (d,),
-              f"bias: expected {weight.dtype} of shape {(d,)}, got {bias.dtype} of {tuple(bias.shape)}")
-    dev = x.device
-    _cuda(dev, x=x, weight=weight, bias=bias)
-    with _scope(dev, stream):
-        y = torch.empty_like(x)
-        mean = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
-        rstd = torch.empty(x.shape[:-1], dtype=_F32, device=dev)
-        _check(moe.lib().moe_layer_norm_forward(
-            x.data_ptr(), weight.data_ptr(), bias.data_ptr() if bias is not None else None, rows, d,
-            x.dtype == _F32, weight.dtype == _F32, eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            _stream(dev)), "moe_layer_norm_forward")
+        if bias.dtype is not weight.dtype or bias.shape != (d,):
+            raise ValueError(f"bias: expected {weight.dtype} of shape {(d,)}, got {bias.dtype} of {tuple(bias.shape)}")
+        bp = _ptr(bias, "bias", index)
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return layer_norm_forward(x, weight, bias, eps)
+    y = torch.empty_like(x)
+    mean = torch.empty(shape[:-1], dtype=_F32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _check(moe.lib().moe_layer_norm_forward(xp, wp, bp, rows, d, x.dtype is _F32, weight.dtype is _F32, eps,
+                                            y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(index)),
+           "moe_layer_norm_forward")
     return y, mean, rstd
+
+
+@functools.lru_cache(maxsize=1024)
+def _ln_workspace_bytes(rows: int, d: int, index: int) -> int:
+    n = ctypes.c_size_t()
+    _check(moe.lib().moe_layer_norm_workspace_bytes(rows, d, ctypes.byref(n)), "moe_layer_norm_workspace_bytes")
+    return n.value
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, need_dx: bool = True, need_dweight: bool = True,
                         need_dbias: bool = True, stream=None):
     """(dx, dweight, dbias) of layer_norm_forward from its saved statistics; None for what is not needed."""
-    rows, d = _ln_args(x, weight)
-    _need(dy is not None and dy.dtype == x.dtype and dy.shape == x.shape,
-          f"dy: expected {x.dtype} of shape {tuple(x.shape)}")
+    shape, rows, d = _ln_args(x, weight)
+    if dy is None or dy.dtype is not x.dtype or dy.shape != shape:
+        raise ValueError(f"dy: expected {x.dtype} of shape {tuple(shape)}")
     for name, s in (("mean", mean), ("rstd", rstd)):
-        _need(s is not None and s.dtype == _F32 and s.shape == x.shape[:-1],
-              f"{name}: expected torch.float32 of shape {tuple(x.shape[:-1])}")
-    dev = x.device
-    _cuda(dev, dy=dy, x=x, weight=weight, mean=mean, rstd=rstd)
-    with _scope(dev, stream):
-        dx = torch.empty_like(x) if need_dx else None
-        dw = torch.empty_like(weight) if need_dweight else None
-        db = torch.empty_like(weight) if need_dbias else None
-        n = ctypes.c_size_t()
-        lib = moe.lib()
-        _check(lib.moe_layer_norm_workspace_bytes(rows, d, ctypes.byref(n)), "moe_layer_norm_workspace_bytes")
-        ws = _workspace(n.value, dev)
-        _check(lib.moe_layer_norm_backward(
-            dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), rows, d,
-            x.dtype == _F32, weight.dtype == _F32, dx.data_ptr() if need_dx else None,
-            dw.data_ptr() if need_dweight else None, db.data_ptr() if need_dbias else None, ws.data_ptr(), n.value,
-            _stream(dev)), "moe_layer_norm_backward")
+        if s is None or s.dtype is not _F32 or s.shape != shape[:-1]:
+            raise ValueError(f"{name}: expected torch.float32 of shape {tuple(shape[:-1])}")
+    index = _device_of(x, "x")
+    args = (_ptr(dy, "dy", index), _ptr(x, "x", index), _ptr(weight, "weight", index), _ptr(mean, "mean", index, 4),
+            _ptr(rstd, "rstd", index, 4))
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return layer_norm_backward(dy, x, weight, mean, rstd, need_dx, need_dweight, need_dbias)
+    dx = torch.empty_like(x) if need_dx else None
+    dw = torch.empty_like(weight) if need_dweight else None
+    db = torch.empty_like(weight) if need_dbias else None
+    n = _ln_workspace_bytes(rows, d, index)
+    ws = _workspace(n, x.device)
+    _check(moe.lib().moe_layer_norm_backward(
+        *args, rows, d, x.dtype is _F32, weight.dtype is _F32, dx.data_ptr() if need_dx else None,
+        dw.data_ptr() if need_dweight else None, db.data_ptr() if need_dbias else None, ws.data_ptr(), n,
+        _raw_stream(index)), "moe_layer_norm_backward")
     return dx, dw, db
 
 
@@ -193,65 +214,45 @@ class LayerNorm(torch.nn.Module):
 # ------------------------------------------------------------------ the loss head
 def _head_args(X, W):
     for name, t in (("X", X), ("W", W)):
-        _need(t is not None and t.dtype == _BF16 and t.dim() == 2, f"{name}: expected a 2-d torch.bfloat16 tensor")
-    _need(X.shape[1] == W.shape[1], f"W: width {W.shape[1]}, X has {X.shape[1]}")
-    return X.shape[0], X.shape[1], W.shape[0]
+        if t is None or t.dtype is not _BF16 or t.dim() != 2:
+            raise ValueError(f"{name}: expected a 2-d torch.bfloat16 tensor")
+    (T, d), (V, dw) = X.shape, W.shape
+    if d != dw:
+        raise ValueError(f"W: width {dw}, X has {d}")
+    return T, d, V
 
 
-def _row_vector(name, t, T):
-    _need(t is not None and t.dtype == _F32 and tuple(t.shape) == (T,),
-          f"{name}: expected torch.float32 of shape {(T,)}")
-
-
-def _ids_arg(name, t, shape):
-    _need(t is not None and t.dtype in (torch.int32, torch.int64) and tuple(t.shape) == shape,
-          f"{name}: expected int32 or int64 of shape {shape}")
+def _label_args(labels, T):
+    if labels is None or (labels.dtype is not _I64 and labels.dtype is not _I32) or labels.shape != (T,):
+        raise ValueError(f"labels: expected int32 or int64 of shape {(T,)}")
 
 
 def _teacher_args(teacher, ids, T):
-    _need(teacher is not None and teacher.dtype in (_F32, _BF16) and teacher.dim() == 2 and teacher.shape[0] == T,
-          f"teacher_logits: expected a torch.float32 or torch.bfloat16 tensor of {T} rows")
-    _ids_arg("teacher_ids", ids, tuple(teacher.shape))
+    if teacher is None or (teacher.dtype is not _F32 and teacher.dtype is not _BF16) or teacher.dim() != 2 or \
+            teacher.shape[0] != T:
+        raise ValueError(f"teacher_logits: expected a torch.float32 or torch.bfloat16 tensor of {T} rows")
+    if ids is None or (ids.dtype is not _I64 and ids.dtype is not _I32) or ids.shape != teacher.shape:
+        raise ValueError(f"teacher_ids: expected int32 or int64 of shape {tuple(teacher.shape)}")
 
 
-def _head_config(T, d, V, ids, teacher=None, temperature=1.0, piece=0, wait_timeout_ns=0, debug_flags=0):
-    return moe_head_config_t(T, V, d, teacher.shape[1] if teacher is not None else 0, temperature,
-                             ids.dtype == torch.int64, teacher is not None and teacher.dtype == _BF16, piece,
-                             wait_timeout_ns, debug_flags)
+def _row_vectors(T, dloss, lse):
+    for name, t in (("dloss", dloss), ("lse", lse)):
+        if t is None or t.dtype is not _F32 or t.shape != (T,):
+            raise ValueError(f"{name}: expected torch.float32 of shape {(T,)}")
 
 
-def _head_workspace(cfg, distill: bool, backward: bool, device):
+@functools.lru_cache(maxsize=1024)
+def _head_workspace_bytes(T, V, d, K, piece, backward, index) -> int:
+    """K = 0: cross entropy."""
+    cfg = moe_head_config_t(T, V, d, K, 1.0, 0, 0, piece, 0, 0)
     n = ctypes.c_size_t()
-    _check(moe.lib().moe_head_workspace_bytes(ctypes.byref(cfg), distill, backward, ctypes.byref(n)),
+    _check(moe.lib().moe_head_workspace_bytes(ctypes.byref(cfg), K > 0, backward, ctypes.byref(n)),
            "moe_head_workspace_bytes")
-    return _workspace(n.value, device), n.value
+    return n.value
 
 
-def _head_forward(name, X, W, targets, cfg, distill, stream):
-    dev = X.device
-    with _scope(dev, stream):
-        out = torch.empty((2, X.shape[0]), dtype=_F32, device=dev)
-        loss, lse = out[0], out[1]
-        ws, n = _head_workspace(cfg, distill, False, dev)
-        status = _status_word(dev)
-        _check(getattr(moe.lib(), name)(ctypes.byref(cfg), X.data_ptr(), W.data_ptr(),
-                                        *[t.data_ptr() for t in targets], loss.data_ptr(), lse.data_ptr(),
-                                        ws.data_ptr(), n, status.data_ptr(), _stream(dev)), name)
-    return loss, lse
-
-
-def _head_backward(name, dloss, X, W, targets, lse, cfg, distill, need_dX, need_dW, stream):
-    dev = X.device
-    with _scope(dev, stream):
-        dX = torch.empty_like(X) if need_dX else None
-        dW = torch.empty_like(W) if need_dW else None
-        ws, n = _head_workspace(cfg, distill, True, dev)
-        status = _status_word(dev)
-        _check(getattr(moe.lib(), name)(ctypes.byref(cfg), dloss.data_ptr(), X.data_ptr(), W.data_ptr(),
-                                        *[t.data_ptr() for t in targets], lse.data_ptr(),
-                                        dX.data_ptr() if need_dX else None, dW.data_ptr() if need_dW else None,
-                                        ws.data_ptr(), n, status.data_ptr(), _stream(dev)), name)
-    return dX, dW
+def _ids_align(t) -> int:
+    return 8 if t.dtype is _I64 else 4
 
 
 def cross_entropy_forward(X, W, labels, stream=None, wait_timeout_ns: int = 0, debug_flags: int = 0):
@@ -260,11 +261,25 @@ def cross_entropy_forward(X, W, labels, stream=None, wait_timeout_ns: int = 0, d
     X bf16 [T, d], W bf16 [V, d], d a multiple of 8; labels int32 or int64
     [T].  A label outside [0, V) marks a token without a loss (0, and lse 0)."""
     T, d, V = _head_args(X, W)
-    _ids_arg("labels", labels, (T,))
-    dev = X.device
-    _cuda(dev, X=X, W=W, labels=labels)
-    cfg = _head_config(T, d, V, labels, wait_timeout_ns=wait_timeout_ns, debug_flags=debug_flags)
-    return _head_forward("moe_cross_entropy_forward", X, W, (labels,), cfg, False, stream)
+    _label_args(labels, T)
+    index = _device_of(X, "X")
+    args = (_ptr(X, "X", index), _ptr(W, "W", index), _ptr(labels, "labels", index, _ids_align(labels)))
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return cross_entropy_forward(X, W, labels, None, wait_timeout_ns, debug_flags)
+    cfg = moe_head_config_t(T, V, d, 0, 1.0, labels.dtype is _I64, 0, 0, wait_timeout_ns, debug_flags)
+    return _head_forward(moe.lib().moe_cross_entropy_forward, "moe_cross_entropy_forward", cfg, X, args, index)
+
+
+def _head_forward(call, name, cfg, X, args, index):
+    loss = torch.empty(cfg.T, dtype=_F32, device=X.device)
+    lse = torch.empty_like(loss)
+    n = _head_workspace_bytes(cfg.T, cfg.V, cfg.d, cfg.K, 0, False, index)
+    ws = _workspace(n, X.device)
+    _check(call(ctypes.byref(cfg), *args, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n,
+                _status_word(index).data_ptr(), _raw_stream(index)), name)
+    return loss, lse
 
 
 def cross_entropy_backward(dloss, X, W, labels, lse, need_dX: bool = True, need_dW: bool = True, piece: int = 0,
@@ -274,14 +289,29 @@ def cross_entropy_backward(dloss, X, W, labels, lse, need_dX: bool = True, need_
     `piece`: vocabulary columns handled at a time (0: a default that keeps
     the piece's workspace near 256 MB)."""
     T, d, V = _head_args(X, W)
-    _ids_arg("labels", labels, (T,))
-    _row_vector("dloss", dloss, T)
-    _row_vector("lse", lse, T)
-    _cuda(X.device, X=X, W=W, labels=labels)
-    _rows_on(X.device, dloss=dloss, lse=lse)
-    cfg = _head_config(T, d, V, labels, piece=piece, wait_timeout_ns=wait_timeout_ns, debug_flags=debug_flags)
-    return _head_backward("moe_cross_entropy_backward", dloss, X, W, (labels,), lse, cfg, False, need_dX, need_dW,
-                          stream)
+    _label_args(labels, T)
+    _row_vectors(T, dloss, lse)
+    index = _device_of(X, "X")
+    args = (_ptr(dloss, "dloss", index, 4), _ptr(X, "X", index), _ptr(W, "W", index),
+            _ptr(labels, "labels", index, _ids_align(labels)), _ptr(lse, "lse", index, 4))
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return cross_entropy_backward(dloss, X, W, labels, lse, need_dX, need_dW, piece, None, wait_timeout_ns,
+                                          debug_flags)
+    cfg = moe_head_config_t(T, V, d, 0, 1.0, labels.dtype is _I64, 0, piece, wait_timeout_ns, debug_flags)
+    return _head_backward(moe.lib().moe_cross_entropy_backward, "moe_cross_entropy_backward", cfg, X, W, args, need_dX,
+                          need_dW, index)
+
+
+def _head_backward(call, name, cfg, X, W, args, need_dX, need_dW, index):
+    dX = torch.empty_like(X) if need_dX else None
+    dW = torch.empty_like(W) if need_dW else None
+    n = _head_workspace_bytes(cfg.T, cfg.V, cfg.d, cfg.K, cfg.piece, True, index)
+    ws = _workspace(n, X.device)
+    _check(call(ctypes.byref(cfg), *args, dX.data_ptr() if need_dX else None, dW.data_ptr() if need_dW else None,
+                ws.data_ptr(), n, _status_word(index).data_ptr(), _raw_stream(index)), name)
+    return dX, dW
 
 
 def distill_forward(X, W, teacher_logits, teacher_ids, temperature: float = 1.0, stream=None,
@@ -293,10 +323,17 @@ def distill_forward(X, W, teacher_logits, teacher_ids, temperature: float = 1.0,
     entry whose id is outside [0, V) or whose logit is -inf is not in use."""
     T, d, V = _head_args(X, W)
     _teacher_args(teacher_logits, teacher_ids, T)
-    _cuda(X.device, X=X, W=W, teacher_logits=teacher_logits, teacher_ids=teacher_ids)
-    cfg = _head_config(T, d, V, teacher_ids, teacher_logits, temperature, wait_timeout_ns=wait_timeout_ns,
-                       debug_flags=debug_flags)
-    return _head_forward("moe_distill_forward", X, W, (teacher_logits, teacher_ids), cfg, True, stream)
+    index = _device_of(X, "X")
+    args = (_ptr(X, "X", index), _ptr(W, "W", index),
+            _ptr(teacher_logits, "teacher_logits", index, teacher_logits.element_size()),
+            _ptr(teacher_ids, "teacher_ids", index, _ids_align(teacher_ids)))
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return distill_forward(X, W, teacher_logits, teacher_ids, temperature, None, wait_timeout_ns, debug_flags)
+    cfg = moe_head_config_t(T, V, d, teacher_ids.shape[1], temperature, teacher_ids.dtype is _I64,
+                            teacher_logits.dtype is _BF16, 0, wait_timeout_ns, debug_flags)
+    return _head_forward(moe.lib().moe_distill_forward, "moe_distill_forward", cfg, X, args, index)
 
 
 def distill_backward(dloss, X, W, teacher_logits, teacher_ids, lse, temperature: float = 1.0, need_dX: bool = True,
@@ -305,19 +342,20 @@ def distill_backward(dloss, X, W, teacher_logits, teacher_ids, lse, temperature:
     """(dX, dW) bf16 of distill_forward for the upstream gradient dloss fp32 [T]; None for what is not needed."""
     T, d, V = _head_args(X, W)
     _teacher_args(teacher_logits, teacher_ids, T)
-    _row_vector("dloss", dloss, T)
-    _row_vector("lse", lse, T)
-    _cuda(X.device, X=X, W=W, teacher_logits=teacher_logits, teacher_ids=teacher_ids)
-    _rows_on(X.device, dloss=dloss, lse=lse)
-    cfg = _head_config(T, d, V, teacher_ids, teacher_logits, temperature, piece, wait_timeout_ns, debug_flags)
-    return _head_backward("moe_distill_backward", dloss, X, W, (teacher_logits, teacher_ids), lse, cfg, True, need_dX,
-                          need_dW, stream)
-
-
-def _rows_on(device, **vectors) -> None:
-    """Row vectors need no more than their own alignment (a row of a larger tensor is fine)."""
-    for name, t in vectors.items():
-        _need(t.is_cuda and t.device == device and t.is_contiguous(), f"{name}: must be contiguous on {device}")
+    _row_vectors(T, dloss, lse)
+    index = _device_of(X, "X")
+    args = (_ptr(dloss, "dloss", index, 4), _ptr(X, "X", index), _ptr(W, "W", index),
+            _ptr(teacher_logits, "teacher_logits", index, teacher_logits.element_size()),
+            _ptr(teacher_ids, "teacher_ids", index, _ids_align(teacher_ids)), _ptr(lse, "lse", index, 4))
+    there = _elsewhere(index, stream)
+    if there is not None:
+        with there:
+            return distill_backward(dloss, X, W, teacher_logits, teacher_ids, lse, temperature, need_dX, need_dW, piece,
+                                    None, wait_timeout_ns, debug_flags)
+    cfg = moe_head_config_t(T, V, d, teacher_ids.shape[1], temperature, teacher_ids.dtype is _I64,
+                            teacher_logits.dtype is _BF16, piece, wait_timeout_ns, debug_flags)
+    return _head_backward(moe.lib().moe_distill_backward, "moe_distill_backward", cfg, X, W, args, need_dX, need_dW,
+                          index)
 
 
 class _CrossEntropyFunction(torch.autograd.Function):
