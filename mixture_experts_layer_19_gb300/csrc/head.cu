@@ -80,21 +80,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// Row-major [rows, cols] with row stride ld (elements), box [box_r, box_c].
-bool tmap(CUtensorMap* m, const void* base, int esize, int64_t cols, int64_t rows, int64_t ld, int box_c, int box_r,
-          CUtensorMapSwizzle sw) {
+// bf16, row-major [rows, cols] with row stride ld: boxes of 64 columns (128
+// bytes, 128-byte swizzle) and box_r rows; reads past the edges give zeros.
+bool map_k(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_r) {
   auto enc = encoder();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)ld * esize};
-  cuuint32_t box[2] = {(cuuint32_t)box_c, (cuuint32_t)box_r};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_r};
   cuuint32_t es[2] = {1, 1};
-  return enc(m, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-             const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-bool map_k(CUtensorMap* m, const void* b, int64_t cols, int64_t rows, int64_t ld, int box_r) {
-  return tmap(m, b, 2, cols, rows, ld, 64, box_r, CU_TENSOR_MAP_SWIZZLE_128B);
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -104,7 +101,8 @@ struct Layout {
   int K, nsplit;
   bool pair_z, pair_x, pair_w;   // CTA pairs for the logits, dX and dW products
   bool sums;                // dX needs the fp32 sums (several pieces or splits)
-  size_t counts, scale, rowmap, inv, ids, probs, cnt, plogp, xc, part, zt, dl, acc, total;
+  int64_t blocks;           // blocks of 128 vocabulary columns
+  size_t counts, scale, rec, inv, ids, probs, first, cnt, plogp, xc, part, zt, dl, acc, total;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -161,9 +159,11 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
   };
   L.counts = take(16);
   L.scale = take(4);
-  L.rowmap = take(L.Tp * 4);
+  L.rec = take(L.Tp * 16);
   L.inv = take(c.T * 4);
-  L.ids = take((size_t)c.T * L.K * 4);
+  L.blocks = 2 * ceil_div(c.V, kHeadBN);
+  L.ids = distill ? take((size_t)c.T * L.K * 4) : 0;
+  L.first = distill ? take((size_t)c.T * L.blocks * 2) : 0;
   L.probs = distill ? take((size_t)c.T * L.K * 4) : 0;
   L.cnt = distill ? take(c.T * 4) : 0;
   L.plogp = distill ? take(c.T * 4) : 0;
@@ -184,10 +184,12 @@ HeadRows rows_of(const Layout& L, void* ws, bool distill) {
   HeadRows r{};
   r.n_active = reinterpret_cast<int32_t*>(b + L.counts);
   r.scale = reinterpret_cast<float*>(b + L.scale);
-  r.rowmap = reinterpret_cast<int32_t*>(b + L.rowmap);
+  r.rec = reinterpret_cast<int4*>(b + L.rec);
   r.inv = reinterpret_cast<int32_t*>(b + L.inv);
-  r.ids = reinterpret_cast<int32_t*>(b + L.ids);
+  r.blocks = L.blocks;
   if (distill) {
+    r.ids = reinterpret_cast<int32_t*>(b + L.ids);
+    r.first = reinterpret_cast<uint16_t*>(b + L.first);
     r.probs = reinterpret_cast<float*>(b + L.probs);
     r.cnt = reinterpret_cast<int32_t*>(b + L.cnt);
     r.plogp = reinterpret_cast<float*>(b + L.plogp);
@@ -264,12 +266,11 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
 
   HeadArgs a{};
   a.n_active = r.n_active;
-  a.rowmap = r.rowmap;
+  a.rec = r.rec;
   a.ids = r.ids;
   a.probs = r.probs;
-  a.cnt = r.cnt;
-  a.lse = h.lse_in;
-  a.dloss = h.dloss;
+  a.first = r.first;
+  a.blocks = L.blocks;
   a.scale = r.scale;
   a.part = r.part;
   a.zt = r.zt;
@@ -289,17 +290,16 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
             map_k(&a.mapB0, h.W, c.d, c.V, c.d, L.pair_z ? 128 : 256);
   HeadArgs ax{}, aw{};
   if (backward) {
-    ok = ok && tmap(&a.mapO, r.dl, 2, L.ldl, L.Tp, L.ldl, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    a.dl = static_cast<__nv_bfloat16*>(r.dl);
+    a.ldl = L.ldl;
     ax = a;
     ax.nsplit = L.nsplit;
     ax.acc = r.acc;
     ok = ok && map_k(&ax.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 128) && map_k(&ax.mapB0, h.W, c.d, c.V, c.d, 64);
-    if (L.sums)
-      ok = ok && tmap(&ax.mapO, r.acc, 4, c.d, (int64_t)L.nsplit * L.Tp, c.d, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     aw = a;
+    aw.dW = static_cast<__nv_bfloat16*>(h.dW);
     ok = ok && map_k(&aw.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 64) && map_k(&aw.mapB0, h.X, c.d, T, c.d, 64) &&
          map_k(&aw.mapB1, r.Xc, c.d, L.Tp, c.d, 64);
-    if (h.dW) ok = ok && tmap(&aw.mapO, h.dW, 2, c.d, c.V, c.d, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (!ok) return bad(w, "tensor map encoding failed", MOE_ERR_CUDA);
 
@@ -308,7 +308,7 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   if (distill)
     e = launch_head_entries(h.teacher, c.teacher_bf16 != 0, h.ids, c.ids_int64 != 0, T, L.K, c.V, a.inv_temp, r, h.st);
   if (e == cudaSuccess)
-    e = launch_head_prep(h.labels, c.ids_int64 != 0, h.dloss, h.X, T, c.d, c.V, r, backward ? h.dX : nullptr, f.sms,
+    e = launch_head_prep(h.labels, c.ids_int64 != 0, h.dloss, h.lse_in, h.X, T, c.d, c.V, r, backward ? h.dX : nullptr, f.sms,
                          h.st);
   if (e != cudaSuccess) return cuda_bad(w, "row kernels", e);
 

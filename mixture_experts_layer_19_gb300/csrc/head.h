@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 namespace moe {
@@ -23,19 +24,21 @@ struct HeadArgs {
   CUtensorMap mapA1;         // kHeadLse / kHeadDl: the compacted copy of X
   CUtensorMap mapB0;         // B operand; kHeadDW: X itself
   CUtensorMap mapB1;         // kHeadDW: the compacted copy of X
-  CUtensorMap mapO;          // stores: dl piece, fp32 dX sums, dW
   const int32_t* n_active;   // [1] compact rows
-  const int32_t* rowmap;     // [Tp] token of each compact row
-  const int32_t* ids;        // [T, K] target entries of each token, ascending
-  const float* probs;        // [T, K] their probabilities, NULL = 1
-  const int32_t* cnt;        // [T] entries in use, NULL = K
-  const float* lse;          // kHeadDl: [T] saved log-sum-exp (of the logits over the temperature)
-  const float* dloss;        // kHeadDl: [T] upstream gradient
+  const int4* rec;           // [Tp] of each compact row: token, label (or teacher entries in use), and, as float
+                             //   bits for kHeadDl, log-sum-exp in base 2 and upstream gradient / *scale
+  const int32_t* ids;        // distillation: [T, K] entries in use of each token, ids ascending
+  const float* probs;        // [T, K] their probabilities
+  const uint16_t* first;     // [T, blocks] first entry at or past vocabulary column 128 * block; NULL: labels
+  int64_t blocks;
   const float* scale;        // [1] common factor of dloss, taken out of D and applied to the sums
   float2* part;              // kHeadLse: [2 * NT, Tp] (max, sum of exp) of 128 columns of one row
   float* zt;                 // kHeadLse: [T, K] logits at the target entries
-  const float* acc;          // kHeadDX: the fp32 sums mapO stores to
+  __nv_bfloat16* dl;         // kHeadDl: [Tp, ldl] this piece of D
+  int64_t ldl;
+  float* acc;                // kHeadDX: [nsplit, Tp, d] fp32 sums
   __nv_bfloat16* dX;         // kHeadDX: [T, d], written instead of the sums (last piece, nsplit = 1); else NULL
+  __nv_bfloat16* dW;         // kHeadDW: [V, d]
   int32_t* status;
   uint64_t timeout_ns;
   int64_t Tp;                // padded rows of the compact buffers
@@ -58,10 +61,12 @@ cudaError_t head_gemm_max_pairs(int* pairs);
 struct HeadRows {
   int32_t* n_active;   // [4]
   float* scale;        // [1] common factor of the upstream gradients (backward)
-  int32_t* rowmap;     // [Tp]
+  int4* rec;           // [Tp] see HeadArgs
   int32_t* inv;        // [T] compact row of each token, -1 = inactive
-  int32_t* ids;        // [T, K]
+  int32_t* ids;        // [T, K] (distillation)
   float* probs;        // [T, K] (distillation)
+  uint16_t* first;     // [T, blocks] (distillation)
+  int64_t blocks;
   int32_t* cnt;        // [T]    (distillation)
   float* plogp;        // [T]    (distillation, forward) sum p log p
   void* Xc;            // [Tp, d] bf16
@@ -74,9 +79,9 @@ struct HeadRows {
 cudaError_t launch_head_entries(const void* teacher, bool teacher_bf16, const void* ids, bool ids64, int T, int K,
                                 int64_t V, float inv_temp, const HeadRows& r, cudaStream_t st);
 // The list of rows that count and, when some do not, their compact copy of X.
-// labels != NULL: cross entropy (fills r.ids); otherwise r.cnt says which rows count.
+// labels != NULL: cross entropy; otherwise r.cnt says which rows count.
 // dX != NULL: rows of tokens that do not count are zeroed.
-cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const void* X, int T, int d, int64_t V,
+cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const float* lse, const void* X, int T, int d, int64_t V,
                              const HeadRows& r, void* dX, int num_sms, cudaStream_t st);
 cudaError_t launch_head_loss(int T, int K, int np, int64_t Tp, float temperature, bool distill, const HeadRows& r,
                              float* loss, float* lse, cudaStream_t st);

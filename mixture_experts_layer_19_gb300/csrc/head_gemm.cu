@@ -5,34 +5,39 @@ namespace moe {
 
 namespace {
 
-template <int KIND, int CG>
+template <int KIND, int CG, bool TEACHER>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(head_gemm_kernel<KIND, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(head_gemm_kernel<KIND, CG, TEACHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               HeadTraits<KIND, CG>::smem_bytes);
 }
 
-template <int KIND, int CG>
+template <int KIND, int CG, bool TEACHER>
 cudaError_t launch_one(const HeadArgs& a, int grid, cudaStream_t st) {
-  return launch_pdl(head_gemm_kernel<KIND, CG>, dim3(grid), dim3(kHeadThreads), HeadTraits<KIND, CG>::smem_bytes, st, CG,
-                    a);
+  return launch_pdl(head_gemm_kernel<KIND, CG, TEACHER>, dim3(grid), dim3(kHeadThreads), HeadTraits<KIND, CG>::smem_bytes, st,
+                    CG, a);
 }
 
 template <int CG>
 cudaError_t launch_kind(int kind, const HeadArgs& a, int grid, cudaStream_t st) {
+  const bool teacher = a.first != nullptr;
   switch (kind) {
-    case kHeadLse: return launch_one<kHeadLse, CG>(a, grid, st);
-    case kHeadDl: return launch_one<kHeadDl, CG>(a, grid, st);
-    case kHeadDX: return launch_one<kHeadDX, CG>(a, grid, st);
-    default: return launch_one<kHeadDW, CG>(a, grid, st);
+    case kHeadLse:
+      return teacher ? launch_one<kHeadLse, CG, true>(a, grid, st) : launch_one<kHeadLse, CG, false>(a, grid, st);
+    case kHeadDl:
+      return teacher ? launch_one<kHeadDl, CG, true>(a, grid, st) : launch_one<kHeadDl, CG, false>(a, grid, st);
+    case kHeadDX: return launch_one<kHeadDX, CG, false>(a, grid, st);
+    default: return launch_one<kHeadDW, CG, false>(a, grid, st);
   }
 }
 
 template <int CG>
 cudaError_t prepare_kinds() {
-  cudaError_t e = prepare_one<kHeadLse, CG>();
-  if (e == cudaSuccess) e = prepare_one<kHeadDl, CG>();
-  if (e == cudaSuccess) e = prepare_one<kHeadDX, CG>();
-  if (e == cudaSuccess) e = prepare_one<kHeadDW, CG>();
+  cudaError_t e = prepare_one<kHeadLse, CG, false>();
+  if (e == cudaSuccess) e = prepare_one<kHeadLse, CG, true>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDl, CG, false>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDl, CG, true>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDX, CG, false>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDW, CG, false>();
   return e;
 }
 
@@ -60,7 +65,7 @@ cudaError_t head_gemm_max_pairs(int* pairs) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(pairs, head_gemm_kernel<kHeadDl, 2>, &cfg);
+  return cudaOccupancyMaxActiveClusters(pairs, head_gemm_kernel<kHeadDl, 2, false>, &cfg);
 }
 
 }  // namespace moe

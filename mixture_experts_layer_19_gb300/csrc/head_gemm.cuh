@@ -34,7 +34,6 @@ constexpr int kHBM = 128;                    // rows per CTA
 constexpr int kHBK = 64;                     // K slice (128 bytes of bf16)
 constexpr int kHeadThreads = 320;
 constexpr int kHeadEpiWarps = 8;
-constexpr int kAhead = 2;                    // target entries a row keeps in registers ahead of their columns
 constexpr int kLseChunk = 16;                // K slices per accumulator of kHeadLse (1024)
 
 template <int KIND, int CG>
@@ -46,7 +45,7 @@ struct HeadTraits {
   static constexpr int b_bytes = b_rows * kHBK * 2;           // 32 / 16 KB
   static constexpr int stage_bytes = a_bytes + b_bytes;
   static constexpr int stages = CG == 2 ? 6 : 4;
-  // staging per epilogue warp: 32 rows of 128 bytes (64 bf16 or 32 fp32 columns)
+  // staging per epilogue warp: 32 rows of 128 bytes
   static constexpr int staging = KIND == kHeadLse ? 0 : 4096;
   static constexpr int smem_bytes = stages * stage_bytes + kHeadEpiWarps * staging + 1024 + 256;
 };
@@ -178,42 +177,86 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// TMA store / fp32 reduce of one staged 32 x 32 block.
-__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* m, const void* src, int32_t x, int32_t y) {
-  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(x), "r"(y), "r"(smem_u32(src))
-               : "memory");
-}
-// Blocks for 128-byte-swizzled stores: 16-byte chunk c of row r at c ^ (r & 7).
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
-// 32 of a row's 64 bf16 columns: the first half or the second.
-__device__ __forceinline__ void head_stage_bf16(uint8_t* buf, int lane, int half, const float* v) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4*>(buf + lane * 128 + (((half * 4 + c) ^ (lane & 7)) << 4)) = pack8(v + 8 * c);
+// An epilogue warp's lanes hold one row each; rows are transposed through 32
+// x 128 bytes of shared memory so that eight lanes write a row's 128 bytes
+// together.  (TMA stores of the same blocks cost a proxy fence and a wait per block:
+// the fences alone were a fifth of these warps' time.)  16-byte chunk c
+// of row r sits at c ^ (r & 7).
+__device__ __forceinline__ void stage_put(uint8_t* buf, int lane, int c, uint4 v) {
+  *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
 }
-__device__ __forceinline__ void head_stage_f32(uint8_t* buf, int lane, const uint32_t* v) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+__device__ __forceinline__ uint4 stage_get(const uint8_t* buf, int r, int c) {
+  return *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
 }
 
-// First entry of an ascending list that is >= key.
-__device__ __forceinline__ int lower_bound_i32(const int32_t* a, int n, int64_t key) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if ((int64_t)__ldg(a + mid) < key) lo = mid + 1;
-    else hi = mid;
+// What an epilogue lane needs to know about its row and the row's target
+// entries inside its 128 columns.  The next tile's are fetched while the
+// current one is worked on, in the three dependent steps below.
+template <bool TEACHER>
+struct HeadRow {
+  int tok;             // token, -1 past the rows that count
+  int cnt;             // TEACHER: entries in use; else the label
+  float rl, gr;        // kHeadDl: log-sum-exp in base 2, upstream gradient over the common factor
+  int e;               // next entry
+  int id0, id1;        // next two entries' vocabulary ids, INT_MAX past the list
+  float p0, p1;
+
+  __device__ __forceinline__ void fetch_record(const HeadArgs& g, int64_t row, int na) {
+    int4 q = make_int4(-1, 0, 0, 0);
+    if (row < na) q = __ldg(g.rec + row);
+    tok = q.x;
+    cnt = q.y;
+    rl = __int_as_float(q.z);
+    gr = __int_as_float(q.w);
   }
-  return lo;
+  __device__ __forceinline__ void find_first(const HeadArgs& g, int64_t vcol) {
+    if constexpr (TEACHER) e = tok >= 0 ? (int)__ldg(g.first + (int64_t)tok * g.blocks + vcol / 128) : 0;
+  }
+  __device__ __forceinline__ void load(const HeadArgs& g, int i, int& id, float& p) {
+    const bool in = tok >= 0 && i < cnt;
+    id = in ? __ldg(g.ids + (int64_t)tok * g.K + i) : INT_MAX;
+    p = in ? __ldg(g.probs + (int64_t)tok * g.K + i) : 0.0f;
+  }
+  __device__ __forceinline__ void fetch_entries(const HeadArgs& g, int64_t vcol) {
+    if constexpr (TEACHER) {
+      load(g, e, id0, p0);
+      load(g, e + 1, id1, p1);
+    } else {
+      e = 0;
+      id0 = tok >= 0 && cnt >= vcol ? cnt : INT_MAX;
+      p0 = 1.0f;
+    }
+  }
+  __device__ __forceinline__ void next(const HeadArgs& g) {
+    ++e;
+    if constexpr (TEACHER) {
+      id0 = id1;
+      p0 = p1;
+      load(g, e + 1, id1, p1);
+    } else {
+      id0 = INT_MAX;
+    }
+  }
+};
+
+// v[col] of 32 registers: 31 selections by the bits of col.
+__device__ __forceinline__ float pick32(const float* v, int col) {
+  float t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t[i] = (col & 1) ? v[2 * i + 1] : v[2 * i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = (col & 2) ? t[2 * i + 1] : t[2 * i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = (col & 4) ? t[2 * i + 1] : t[2 * i];
+  t[0] = (col & 8) ? t[1] : t[0];
+  t[2] = (col & 8) ? t[3] : t[2];
+  return (col & 16) ? t[2] : t[0];
 }
 
-template <int KIND, int CG>
+template <int KIND, int CG, bool TEACHER>
 __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid_constant__ HeadArgs g) {
   using TR = HeadTraits<KIND, CG>;
   constexpr int kSt = TR::stages;
@@ -274,6 +317,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
+      fence_proxy_async_global();                       // the predecessors' plain stores, read by TMA below
       const uint64_t pol = policy_evict_last();
       const bool all = na == g.T;                       // no row skipped: X is read in place
       const CUtensorMap* mA = (KIND <= kHeadDl && !all) ? &g.mapA1 : &g.mapA0;
@@ -387,39 +431,37 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         else mbar_arrive_cluster(mapa_u32(smem_u32(&tempty[a]), 0));
       }
     };
+    const uint32_t lane_off = (uint32_t)(32 * q) << 16;
+    const int sub = lane >> 3, chunk = lane & 7;                  // coalesced writes: row within 4, 16-byte chunk
+    [[maybe_unused]] const float sc = KIND >= kHeadDX ? *g.scale * g.out_scale : 1.0f;
+    [[maybe_unused]] HeadRow<TEACHER> cur, nxt;
+    if constexpr (KIND <= kHeadDl) {
+      if (w0 < nwork) {
+        const HeadTile t = head_tile<KIND, CG>(g, na, MT, NT, w0);
+        const int64_t vcol = g.v0 + t.col0 + h * 128;
+        nxt.fetch_record(g, t.row0 + rank * kHBM + 32 * q + lane, na);
+        nxt.find_first(g, vcol);
+        nxt.fetch_entries(g, vcol);
+      }
+    }
     for (int64_t w = w0; w < nwork; w += wstep) {
       const HeadTile t = head_tile<KIND, CG>(g, na, MT, NT, w);
-      const int64_t row = t.row0 + rank * kHBM + 32 * q + lane;   // this lane's row
-      const int64_t rowq = row - lane;                            // the warp's first row
+      const int64_t rowq = t.row0 + rank * kHBM + 32 * q;         // the warp's first row
+      const int64_t row = rowq + lane;                            // this lane's row
       const int64_t colh = t.col0 + h * 128;                      // the warp's first column
-      const uint32_t lane_off = (uint32_t)(32 * q) << 16;
 
-      if constexpr (KIND == kHeadLse || KIND == kHeadDl) {
-        const bool live = row < na;
-        const int64_t tok = live ? g.rowmap[row] : 0;
-        const int32_t* ids = g.ids + tok * g.K;
-        const int cnt = live ? (g.cnt ? g.cnt[tok] : g.K) : 0;
+      if constexpr (KIND <= kHeadDl) {
+        cur = nxt;
         const int64_t vcol = g.v0 + colh;                         // vocabulary id of the first column
-        int e = lower_bound_i32(ids, cnt, vcol);
-        // the row's next entries, read before the products are waited for
-        int64_t nid[kAhead];
-        float np[kAhead];
-        auto entry = [&](int i, int64_t& id, float& p) {
-          const bool in = i < cnt;
-          id = in ? (int64_t)__ldg(ids + i) : INT64_MAX;
-          p = (KIND == kHeadDl && in && g.probs) ? __ldg(g.probs + tok * g.K + i) : 1.0f;
-        };
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) entry(e + i, nid[i], np[i]);
-        auto next_entry = [&]() {
-          ++e;
-#pragma unroll
-          for (int i = 0; i + 1 < kAhead; ++i) {
-            nid[i] = nid[i + 1];
-            np[i] = np[i + 1];
-          }
-          entry(e + kAhead - 1, nid[kAhead - 1], np[kAhead - 1]);
-        };
+        const bool more = w + wstep < nwork;
+        int64_t nvcol = 0;
+        if (more) {
+          const HeadTile n = head_tile<KIND, CG>(g, na, MT, NT, w + wstep);
+          nvcol = g.v0 + n.col0 + h * 128;
+          nxt.fetch_record(g, n.row0 + rank * kHBM + 32 * q + lane, na);
+        }
+        const int64_t left = g.vlen - colh;                       // columns inside the vocabulary
+        const int last = (int)vcol + 128;                         // ids below it are this block's
         if constexpr (KIND == kHeadLse) {
           float z[128];
           const int phases = head_phases<KIND>(t.nkb);
@@ -446,21 +488,20 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
             if (acc == 0) aph ^= 1;
           }
           if (!ok) break;
+          if (more) nxt.find_first(g, nvcol);
           // logits at this row's target entries inside these 128 columns
-          while (true) {
-            const bool hit = nid[0] < vcol + 128;
-            if (!__any_sync(0xffffffffu, hit)) break;
-            const int col = hit ? (int)(nid[0] - vcol) : -1;
-            float v = 0.0f;
+          while (__any_sync(0xffffffffu, cur.id0 < last)) {
+            const int col = (cur.id0 - (int)vcol) & 127;
+            float v[4];
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i == col) v = z[i];
-            if (hit) {
-              g.zt[tok * g.K + e] = v;
-              next_entry();
+            for (int c = 0; c < 4; ++c) v[c] = pick32(z + c * 32, col);
+            const float lo = (col & 32) ? v[1] : v[0], hi = (col & 32) ? v[3] : v[2];
+            if (cur.id0 < last) {
+              g.zt[(int64_t)cur.tok * g.K + cur.e] = (col & 64) ? hi : lo;
+              cur.next(g);
             }
           }
-          const int64_t left = g.vlen - colh;
+          if (more) nxt.fetch_entries(g, nvcol);
           if (left < 128) {
 #pragma unroll
             for (int i = 0; i < 128; ++i)
@@ -474,132 +515,142 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int i = 0; i < 128; ++i) s4[i & 3] += ex2_approx(fmaf(z[i], c2, -mb));
-          if (row < g.Tp)
-            g.part[(2 * (t.col0 / kHeadBN) + h) * g.Tp + row] =
-                make_float2(m * g.inv_temp, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+          g.part[(2 * (t.col0 / kHeadBN) + h) * g.Tp + row] =
+              make_float2(m * g.inv_temp, (s4[0] + s4[1]) + (s4[2] + s4[3]));
         } else {
-          const float rl = live ? g.lse[tok] * 1.4426950408889634f : 0.0f;
-          float gr = 0.0f;
-          if (live) gr = g.dloss[tok] / *g.scale;
           if (!mbar_wait(&tfull[acc], aph, wc)) break;
           tc_fence_after();
           const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * 128;
-#pragma unroll 1
+          uint32_t r[32];
+          tmem_ld32(tb, r);
+          __nv_bfloat16* out = g.dl + (rowq + sub) * g.ldl + colh + chunk * 8;
+#pragma unroll
           for (int c = 0; c < 4; ++c) {                           // 32 columns at a time, stored by 64
-            uint32_t r[32];
-            tmem_ld32(tb + c * 32, r);
             tmem_ld_wait();
-            if (c == 3) release(acc);
             float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = ex2_approx(fmaf(__uint_as_float(r[i]), c2, -rl));
-            while (true) {
-              const bool hit = nid[0] < vcol + c * 32 + 32;
-              if (!__any_sync(0xffffffffu, hit)) break;
-              const int col = hit ? (int)(nid[0] - vcol) - c * 32 : -1;
-              const float p = np[0];
+            for (int i = 0; i < 32; ++i) v[i] = ex2_approx(fmaf(__uint_as_float(r[i]), c2, -cur.rl));
+            if (c < 3) tmem_ld32(tb + (c + 1) * 32, r);
+            else release(acc);
+            while (__any_sync(0xffffffffu, cur.id0 < last - 96 + c * 32)) {
+              const bool hit = cur.id0 < last - 96 + c * 32;
+              const int col = hit ? cur.id0 - (int)vcol - c * 32 : -1;
+              const float p = cur.p0;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (i == col) v[i] -= p;
-              if (hit) next_entry();
+              if (hit) cur.next(g);
             }
-            const int64_t left = g.vlen - colh - c * 32;          // columns past the vocabulary are zeros
+            if (c == 1 && more) nxt.find_first(g, nvcol);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = (live && i < left) ? v[i] * gr : 0.0f;
-            if (!(c & 1)) {
-              if (lane == 0) bulk_wait_read<0>();
-              __syncwarp();
+            for (int i = 0; i < 32; ++i) v[i] *= cur.gr;
+            if (left < 128 || rowq + 32 > na) {                   // zeros past the vocabulary and the rows that count
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i >= left || cur.tok < 0) v[i] = 0.0f;
             }
-            head_stage_bf16(stg, lane, c & 1, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) stage_put(stg, lane, (c & 1) * 4 + k, pack8(v + 8 * k));
             if (c & 1) {
-              fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0) {
-                tma_store_2d(&g.mapO, stg, (int32_t)(colh + (c - 1) * 32), (int32_t)rowq);
-                bulk_commit();
-              }
+#pragma unroll
+              for (int it = 0; it < 8; ++it)
+                *reinterpret_cast<uint4*>(out + (int64_t)(4 * it) * g.ldl + (c - 1) * 32) =
+                    stage_get(stg, 4 * it + sub, chunk);
+              __syncwarp();
             }
           }
+          if (more) nxt.fetch_entries(g, nvcol);
           acc ^= 1;
           if (acc == 0) aph ^= 1;
         }
       } else {
         const bool has = t.nkb > 0;
+        const bool final_dx = KIND == kHeadDX && g.dX != nullptr;
+        int tok = -1;
+        if (final_dx && row < na) tok = __ldg(g.rec + row).x;
         if (has) {
           if (!mbar_wait(&tfull[acc], aph, wc)) break;
           tc_fence_after();
         }
         const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * 128;
-        const float sc = *g.scale * g.out_scale;
-        const bool final_dx = KIND == kHeadDX && g.dX != nullptr;
-        const bool live = KIND == kHeadDX && row < na;
-        const int64_t tok = final_dx && live ? g.rowmap[row] : 0;
-#pragma unroll 1
+        uint32_t r[32];
+        if (has) {
+          tmem_ld32(tb, r);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          if (has) {
-            tmem_ld32(tb + c * 32, r);
-            tmem_ld_wait();
-            if (c == 3) release(acc);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = 0u;
-          }
+          if (has) tmem_ld_wait();
           const int64_t col = colh + c * 32;
-          if constexpr (KIND == kHeadDX) {
-            if (final_dx) {
-              // last piece, unsplit: add the earlier pieces' sums, round once
-              // and write the token's row
-              if (live) {
+          if (KIND == kHeadDX && !final_dx) {
+            // fp32 sums, 32 columns at a time
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                  if (col + i >= g.d) break;
-                  float v[8];
+            for (int k = 0; k < 8; ++k)
+              stage_put(stg, lane, k, make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]));
+            if (has) {
+              if (c < 3) tmem_ld32(tb + (c + 1) * 32, r);
+              else release(acc);
+            }
+            __syncwarp();
+            if (col + chunk * 4 < g.d) {
+              float* out = g.acc + (t.split * g.Tp + rowq + sub) * g.d + col + chunk * 4;
+              float4 old[8];
+              if (g.add) {
 #pragma unroll
-                  for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[i + j]);
-                  if (g.add) {
-                    const float4* src = reinterpret_cast<const float4*>(g.acc + row * g.d + col + i);
-                    const float4 p = src[0], q4 = src[1];
-                    v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
-                    v[4] += q4.x, v[5] += q4.y, v[6] += q4.z, v[7] += q4.w;
-                  }
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) v[j] *= sc;
-                  *reinterpret_cast<uint4*>(g.dX + tok * g.d + col + i) = pack8(v);
-                }
+                for (int it = 0; it < 8; ++it) old[it] = *reinterpret_cast<const float4*>(out + (int64_t)(4 * it) * g.d);
               }
+#pragma unroll
+              for (int it = 0; it < 8; ++it) {
+                const uint4 u = stage_get(stg, 4 * it + sub, chunk);
+                float4 v = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                       __uint_as_float(u.w));
+                if (g.add) v.x += old[it].x, v.y += old[it].y, v.z += old[it].z, v.w += old[it].w;
+                *reinterpret_cast<float4*>(out + (int64_t)(4 * it) * g.d) = v;
+              }
+            }
+            __syncwarp();
+            continue;
+          }
+          // bf16 results, stored 64 columns at a time
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          if (has) {
+            if (c < 3) tmem_ld32(tb + (c + 1) * 32, r);
+            else release(acc);
+          }
+          if (KIND == kHeadDX && g.add && tok >= 0) {             // the earlier pieces' sums
+            const float4* src = reinterpret_cast<const float4*>(g.acc + row * g.d + col);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (col + 4 * k < g.d) {
+                const float4 o = src[k];
+                v[4 * k] += o.x, v[4 * k + 1] += o.y, v[4 * k + 2] += o.z, v[4 * k + 3] += o.w;
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= sc;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) stage_put(stg, lane, (c & 1) * 4 + k, pack8(v + 8 * k));
+          if (!(c & 1)) continue;
+          __syncwarp();
+          const int64_t x = col - 32 + chunk * 8;
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            const int rr = 4 * it + sub;
+            const uint4 u = stage_get(stg, rr, chunk);
+            if constexpr (KIND == kHeadDX) {
+              const int to = __shfl_sync(0xffffffffu, tok, rr);
+              if (to >= 0 && x < g.d) *reinterpret_cast<uint4*>(g.dX + (int64_t)to * g.d + x) = u;
             } else {
-              if (lane == 0) bulk_wait_read<0>();
-              __syncwarp();
-              head_stage_f32(stg, lane, r);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0 && col < g.d && rowq < g.Tp) {
-                const int32_t y = (int32_t)(t.split * g.Tp + rowq);
-                if (g.add) tma_reduce_add_2d(&g.mapO, stg, (int32_t)col, y);
-                else tma_store_2d(&g.mapO, stg, (int32_t)col, y);
-                bulk_commit();
-              }
-            }
-          } else {
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = has ? __uint_as_float(r[i]) * sc : 0.0f;
-            if (!(c & 1)) {
-              if (lane == 0) bulk_wait_read<0>();
-              __syncwarp();
-            }
-            head_stage_bf16(stg, lane, c & 1, v);
-            if (c & 1) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                const int64_t x = col - 32;
-                if (x < g.d && rowq < g.vlen) tma_store_2d(&g.mapO, stg, (int32_t)x, (int32_t)(g.v0 + rowq));
-                bulk_commit();
-              }
+              if (rowq + rr < g.vlen && x < g.d)
+                *reinterpret_cast<uint4*>(g.dW + (g.v0 + rowq + rr) * g.d + x) = u;
             }
           }
+          __syncwarp();
         }
         if (has) {
           acc ^= 1;
@@ -607,8 +658,6 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         }
       }
     }
-    if (lane == 0) bulk_wait<0>();
-    __syncwarp();
   }
 
   __syncthreads();

@@ -122,6 +122,15 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const void* teacher, 
     for (int i = 1; i < nw; ++i) h += red[i];
     r.plogp[t] = h;
   }
+  // where each block of 128 vocabulary columns starts in the sorted list
+  for (int64_t b = tid; b < r.blocks; b += nt) {
+    const unsigned long long least = (unsigned long long)(128 * b) << 11;
+    int at = 0;
+    for (int step = Kp2 >> 1; step; step >>= 1)
+      if (key[at + step - 1] < least) at += step;
+    at += at < Kp2 && key[at] < least;
+    r.first[t * r.blocks + b] = (uint16_t)at;
+  }
 }
 
 __device__ __forceinline__ bool row_counts(const void* labels, bool ids64, const float* dloss, int64_t V,
@@ -141,11 +150,10 @@ __device__ __forceinline__ bool row_counts(const void* labels, bool ids64, const
 // follow up to the next multiple of 256.  Every block walks all T tokens to
 // know how many count before its own and in all -- a few bytes per token from L2,
 // less than a second launch would cost -- and then serves its own range.
-// Block 0 also finds (backward) the factor common to the upstream gradients:
-// with one value for all of them (a mean) it is taken out of D before D is
-// rounded to bf16.
-__global__ void __launch_bounds__(256) head_prep_kernel(const void* labels, int ids64, const float* dloss, int T,
-                                                        int64_t V, const uint4* __restrict__ X, int vecs,
+// (Backward) a factor common to all upstream gradients, as in a mean, is
+// taken out of D before D is rounded to bf16.
+__global__ void __launch_bounds__(256) head_prep_kernel(const void* labels, int ids64, const float* dloss,
+                                                        const float* lse, int T, int64_t V, const uint4* __restrict__ X, int vecs,
                                                         HeadRows r, uint4* __restrict__ dX) {
   __shared__ int s_cnt[8][2];
   __shared__ float s_lo[8], s_hi[8];
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(256) head_prep_kernel(const void* labels, int 
     const bool on = row_counts(labels, ids64, dloss, V, r, t);
     total += on;
     before += on && t < t0;
-    if (dloss && on && blockIdx.x == 0) {
+    if (dloss && on) {
       const float gv = dloss[t];
       if (!(fabsf(gv) < CUDART_INF_F)) lo = -CUDART_INF_F;    // not finite: no common factor
       lo = fminf(lo, gv);
@@ -187,13 +195,14 @@ __global__ void __launch_bounds__(256) head_prep_kernel(const void* labels, int 
     before += s_cnt[i][0];
     total += s_cnt[i][1];
   }
+  for (int i = 0; i < 8; ++i) {
+    lo = fminf(lo, s_lo[i]);
+    hi = fmaxf(hi, s_hi[i]);
+  }
+  const float scale = lo == hi && fabsf(lo) < CUDART_INF_F ? lo : 1.0f;
   if (blockIdx.x == 0 && tid == 0) {
-    for (int i = 1; i < 8; ++i) {
-      lo = fminf(lo, s_lo[i]);
-      hi = fmaxf(hi, s_hi[i]);
-    }
     r.n_active[0] = total;
-    *r.scale = lo == hi && fabsf(lo) < CUDART_INF_F ? lo : 1.0f;
+    *r.scale = scale;
   }
   const bool copy = total != T;
   uint4* out = reinterpret_cast<uint4*>(r.Xc);
@@ -209,13 +218,12 @@ __global__ void __launch_bounds__(256) head_prep_kernel(const void* labels, int 
       if (i < warp) at += s_cnt[i][0];
       n += s_cnt[i][0];
     }
-    if (t < t1) {
-      r.inv[t] = on ? before + at : -1;
-      if (labels) r.ids[t] = on ? (int32_t)load_id(labels, ids64, t) : -1;
-    }
+    if (t < t1) r.inv[t] = on ? before + at : -1;
     const int rows = min(256, t1 - base);
     if (on) {
-      r.rowmap[before + at] = t;
+      r.rec[before + at] = make_int4(t, labels ? (int)load_id(labels, ids64, t) : r.cnt[t],
+                                     __float_as_int(dloss ? lse[t] * 1.4426950408889634f : 0.0f),
+                                     __float_as_int(dloss ? dloss[t] / scale : 0.0f));
       s_on[at] = t;
     } else if (t < t1) {
       s_off[tid - at] = t;
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(256) head_dx_kernel(int d, int nsplit, int64_t
       a.z += b.z;
       a.w += b.w;
     }
-    dX[(int64_t)r.rowmap[row] * vecs + c] = make_uint2(pack_bf16(a.x * sc, a.y * sc), pack_bf16(a.z * sc, a.w * sc));
+    dX[(int64_t)r.rec[row].x * vecs + c] = make_uint2(pack_bf16(a.x * sc, a.y * sc), pack_bf16(a.z * sc, a.w * sc));
   }
 }
 
@@ -347,11 +355,11 @@ cudaError_t launch_head_entries(const void* teacher, bool teacher_bf16, const vo
                     (int)ids64, K, kp, V, inv_temp, r);
 }
 
-cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const void* X, int T, int d, int64_t V,
+cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const float* lse, const void* X, int T, int d, int64_t V,
                              const HeadRows& r, void* dX, int num_sms, cudaStream_t st) {
   // few tokens per block, so that a block's copy is short, up to one wave of blocks
   const int blocks = (T + 3) / 4 < 8 * num_sms ? (T + 3) / 4 : 8 * num_sms;
-  return launch_pdl(head_prep_kernel, dim3(blocks), dim3(256), 0, st, 1, labels, (int)ids64, dloss, T, V,
+  return launch_pdl(head_prep_kernel, dim3(blocks), dim3(256), 0, st, 1, labels, (int)ids64, dloss, lse, T, V,
                     reinterpret_cast<const uint4*>(X), d / 8, r, reinterpret_cast<uint4*>(dX));
 }
 
