@@ -146,7 +146,10 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
           L.pair_x = pair != 0;
         }
       }
-    L.pair_w = better_as_pair(cols, c.d, (double)ceil_div(c.T, 64), kEpiGrad, sms, pairs);
+    // dW of few tokens is bound by its writes, which single CTAs, each on its own
+    // tile, keep going better than pairs (64 x 7168 x 131072: 383 us against 503);
+    // from 256 tokens on the products count (875 against 887)
+    L.pair_w = c.T >= 256 && better_as_pair(cols, c.d, (double)ceil_div(c.T, 64), kEpiGrad, sms, pairs);
     L.sums = L.nsplit > 1 || L.piece < c.V;
   }
   L.pair_z = better_as_pair(c.T, backward ? std::min<int64_t>(L.piece, c.V) : c.V, (double)ceil_div(c.d, 64),

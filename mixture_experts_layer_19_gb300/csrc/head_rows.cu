@@ -251,37 +251,56 @@ __global__ void __launch_bounds__(256) head_prep_kernel(const void* labels, int 
   }
 }
 
-// Joins the (max, sum) pairs of a row's 128-column blocks in block order
-// inside 32 slices, then the slices in order, and writes the row's loss.  One block
-// per 32 tokens: lane = token for the join (pairs of neighbouring rows are
-// neighbours in memory), warp = token for the sum over the target entries.
+// (max, sum of exp) of two disjoint sets of columns, joined; (-inf, 0) is the
+// empty set.  A NaN sum stays.
+__device__ __forceinline__ void join(float& m, float& s, float om, float os) {
+  const float mn = fmaxf(m, om);
+  const float a = mn == -CUDART_INF_F ? 0.0f : mn;
+  s = s * expf(m - a) + os * expf(om - a);
+  m = mn;
+}
+
+// Joins the (max, sum) pairs of a token's 128-column blocks and writes its
+// loss.  Four tokens per block (their pairs share a 32-byte sector): each
+// thread joins every 8 * warps-th pair, then threads and warps join in
+// a fixed order; one warp per token then adds up the target entries.
 __global__ void __launch_bounds__(1024) head_loss_kernel(int T, int K, int np, int64_t Tp, float temperature,
                                                          int distill, HeadRows r, float* loss, float* lse) {
-  __shared__ float sm[32][33], ss[32][33];
+  __shared__ float sm[4][32], ss[4][32];
   pdl_wait();
   pdl_release();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int t0 = blockIdx.x * 4;
   {
-    const int t = t0 + lane;
+    const int t = t0 + (lane & 3);
     const int row = t < T ? r.inv[t] : -1;
     float m = -CUDART_INF_F, s = 0.0f;
     if (row >= 0) {
-      const int lo = (int)((int64_t)np * warp / 32), hi = (int)((int64_t)np * (warp + 1) / 32);
-      for (int i = lo; i < hi; ++i) {
-        const float2 p = r.part[i * Tp + row];
-        const float mn = fmaxf(m, p.x);
-        const float a = mn == -CUDART_INF_F ? 0.0f : mn;
-        s = s * expf(m - a) + p.y * expf(p.x - a);
-        m = mn;
+      const float2* src = r.part + row;
+      const int step = 8 * nw;
+      int i = warp * 8 + (lane >> 2);
+      for (; i + 3 * step < np; i += 4 * step) {
+        float2 p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) p[u] = src[(i + u * step) * Tp];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) join(m, s, p[u].x, p[u].y);
       }
+      for (; i < np; i += step) join(m, s, src[i * Tp].x, src[i * Tp].y);
     }
-    sm[warp][lane] = m;
-    ss[warp][lane] = s;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+      join(m, s, om, os);
+    }
+    if (lane < 4) {
+      sm[lane][warp] = m;
+      ss[lane][warp] = s;
+    }
   }
   __syncthreads();
   const int t = t0 + warp;
-  if (t >= T) return;
+  if (warp >= 4 || t >= T) return;
   const int row = r.inv[t];
   if (row < 0) {
     if (lane == 0) {
@@ -290,14 +309,13 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(int T, int K, int np, i
     }
     return;
   }
-  // slice `lane` of token `warp`
-  float m = sm[lane][warp];
-  const float s0 = ss[lane][warp];
-  float mx = m;
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float s = s0 * expf(m - (mx == -CUDART_INF_F ? 0.0f : mx));
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const float l = mx + logf(s);
+  float m = lane < nw ? sm[warp][lane] : -CUDART_INF_F, s = lane < nw ? ss[warp][lane] : 0.0f;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+    join(m, s, om, os);
+  }
+  const float l = m + logf(s);
   const float it = 1.0f / temperature;
   float out;
   if (distill) {
@@ -365,7 +383,8 @@ cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss,
 
 cudaError_t launch_head_loss(int T, int K, int np, int64_t Tp, float temperature, bool distill, const HeadRows& r,
                              float* loss, float* lse, cudaStream_t st) {
-  return launch_pdl(head_loss_kernel, dim3((T + 31) / 32), dim3(1024), 0, st, 1, T, K, np, Tp, temperature, (int)distill,
+  // few blocks: more threads each
+  return launch_pdl(head_loss_kernel, dim3((T + 3) / 4), dim3(T <= 1024 ? 1024 : 256), 0, st, 1, T, K, np, Tp, temperature, (int)distill,
                     r, loss, lse);
 }
 
