@@ -5,10 +5,13 @@
 // its result, so the two passes of the variance -- mean first, then squares
 // about it, which does not cancel as a difference of sums would -- cost no
 // second read.
-//   many rows, forward   one to four warps per row, the row packed in up to 28
-//                        16-byte registers vectors per lane, weights in shared
+//   many rows, forward   one to four warps per row, the row packed in up to 16
+//                        vectors of 16 bytes per lane, weights in shared
 //                        memory; with one warp there is no barrier at all
-//   few rows, odd widths one block per row
+//   narrow rows, forward  several rows per warp, four sets of them in flight
+//   few rows             one block per row
+//   odd widths           one element per access; the backward copies the aligned
+//                        16-byte chunks that cover a row
 //   backward             one block per row; each thread keeps its columns'
 //                        sums of dw and db in registers over all its rows and
 //                        prefetches later rows into its own shared memory
@@ -238,17 +241,20 @@ __device__ __forceinline__ float weight_at(const void* w, bool f32, int i) {
 }
 
 // ---------------------------------------------------------------- forward, many rows
-// wpr warps per row, 12 / wpr rows per block at a time.  Shared memory holds
+// wpr (1, 2, 4) warps per row.  Shared memory holds
 // (w, w, b, b) of each pair of columns, plane by plane so that neighbouring
 // lanes read neighbouring 16 bytes.
-constexpr int kRowWarps = 12;
+// Warps per block (one block per SM): what the registers of NV packed vectors
+// leave room for.
+constexpr int row_warps(int nv) { return nv > 8 ? 16 : nv > 4 ? 24 : 32; }
 template <class XT, int NV>
-__global__ void __launch_bounds__(kRowWarps * 32, 1) ln_fwd_rows_kernel(const uint4* __restrict__ x, const void* w,
+__global__ void __launch_bounds__(row_warps(NV) * 32, 1) ln_fwd_rows_kernel(const uint4* __restrict__ x, const void* w,
                                                                        const void* b, bool w_f32, int64_t rows, int d,
                                                                        int wpr, float eps, uint4* __restrict__ y,
                                                                        float* __restrict__ mean,
                                                                        float* __restrict__ rstd) {
   using P = Pairs<XT>;
+  constexpr int kRowWarps = row_warps(NV);
   extern __shared__ float4 wb[];                         // [P::n][vecs]
   __shared__ float red[2][kRowWarps];
   const int vecs = d / (2 * P::n);
@@ -325,6 +331,84 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) ln_fwd_rows_kernel(const ui
     if (tid == 0) {
       mean[r] = m;
       rstd[r] = rs;
+    }
+  }
+}
+
+// Narrow rows (at most 32 vectors): G lanes per row, 32 / G rows side by side
+// in a warp and four such sets in flight; the weights stay in registers.  One
+// row at a time leaves too few bytes in flight: 46.7 us at 131072 x 256
+// against XX.
+constexpr int kNarrowSets = 4;
+template <class XT>
+__global__ void __launch_bounds__(512, 2) ln_fwd_narrow_kernel(const uint4* __restrict__ x, const void* w,
+                                                               const void* b, bool w_f32, int64_t rows, int d, int G,
+                                                               float eps, uint4* __restrict__ y,
+                                                               float* __restrict__ mean, float* __restrict__ rstd) {
+  using P = Pairs<XT>;
+  const int vecs = d / (2 * P::n), lane = threadIdx.x & 31;
+  const int c = lane & (G - 1), per = 32 / G;
+  const bool in = c < vecs;
+  const float inv_d = 1.0f / (float)d;
+  f2 wr[P::n], br[P::n];
+#pragma unroll
+  for (int p = 0; p < P::n; ++p) {
+    const int e = c * 2 * P::n + 2 * p;
+    wr[p] = in ? f2_make(weight_at(w, w_f32, e), weight_at(w, w_f32, e + 1)) : f2_make(0, 0);
+    br[p] = in && b ? f2_make(weight_at(b, w_f32, e), weight_at(b, w_f32, e + 1)) : f2_make(0, 0);
+  }
+  const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5) * per * kNarrowSets;
+  for (int64_t r0 = warp * per * kNarrowSets + lane / G; r0 - lane / G < rows; r0 += step) {
+    uint4 v[kNarrowSets];
+    float s[kNarrowSets], m[kNarrowSets];
+#pragma unroll
+    for (int u = 0; u < kNarrowSets; ++u) {
+      const int64_t r = r0 + u * per;
+      v[u] = in && r < rows ? __ldcs(x + r * vecs + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kNarrowSets; ++u) {
+      f2 t = P::get(v[u], 0);
+#pragma unroll
+      for (int p = 1; p < P::n; ++p) t = f2_add(t, P::get(v[u], p));
+      const float2 q = f2_get(t);
+      s[u] = q.x + q.y;
+    }
+    for (int o = G >> 1; o; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < kNarrowSets; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+    for (int u = 0; u < kNarrowSets; ++u) {
+      m[u] = s[u] * inv_d;
+      const f2 mm = f2_make(-m[u], -m[u]);
+      f2 t = f2_make(0, 0);
+#pragma unroll
+      for (int p = 0; p < P::n; ++p) {
+        const f2 a = f2_add(P::get(v[u], p), mm);
+        t = f2_fma(a, a, t);
+      }
+      const float2 q = f2_get(t);
+      s[u] = in ? q.x + q.y : 0.0f;
+    }
+    for (int o = G >> 1; o; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < kNarrowSets; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+    for (int u = 0; u < kNarrowSets; ++u) {
+      const int64_t r = r0 + u * per;
+      const float rs = 1.0f / sqrtf(s[u] * inv_d + eps);
+      const f2 rr = f2_make(rs, rs), mm = f2_make(-m[u], -m[u]);
+      if (in && r < rows) {
+        uint4 o;
+#pragma unroll
+        for (int p = 0; p < P::n; ++p) P::set(o, p, f2_fma(f2_mul(f2_add(P::get(v[u], p), mm), rr), wr[p], br[p]));
+        __stcs(y + r * vecs + c, o);
+      }
+      if (c == 0 && r < rows) {
+        mean[r] = m[u];
+        rstd[r] = rs;
+      }
     }
   }
 }
@@ -486,102 +570,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) ln_bwd_rows_kernel(
   }
 }
 
-template <class XT, class WT, int VW, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) ln_bwd_kernel(const XT* __restrict__ dy, const XT* __restrict__ x,
-                                                             const WT* __restrict__ w, const float* __restrict__ mean,
-                                                             const float* __restrict__ rstd, int64_t rows, int d,
-                                                             XT* __restrict__ dx, float* __restrict__ part_w,
-                                                             float* __restrict__ part_b) {
-  using V = Vec<XT, VW>;
-  __shared__ float red[2][16][2];
-  const int vecs = d / VW, nw = blockDim.x >> 5, tid = threadIdx.x;
-  const float inv_d = 1.0f / (float)d;
-  float wr[VPT][VW], aw[VPT][VW], ab[VPT][VW];
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int c = tid + j * blockDim.x;
-#pragma unroll
-    for (int i = 0; i < VW; ++i) wr[j][i] = aw[j][i] = ab[j][i] = 0.0f;
-    if (c < vecs) load_weights<WT, VW>(w + c * VW, wr[j]);
-  }
-  V nx[VPT], ng[VPT];
-  float nm = 0.0f, nr = 0.0f;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j)
-#pragma unroll
-    for (int i = 0; i < VW; ++i) nx[j].v[i] = ng[j].v[i] = from_f<XT>(0.0f);
-  auto fetch = [&](int64_t row) {
-    const V* sx = reinterpret_cast<const V*>(x + row * d);
-    const V* sg = reinterpret_cast<const V*>(dy + row * d);
-    nm = mean[row];
-    nr = rstd[row];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = tid + j * blockDim.x;
-      if (c < vecs) {
-        nx[j] = sx[c];
-        ng[j] = sg[c];
-      }
-    }
-  };
-  int64_t r = blockIdx.x;
-  int flip = 0;
-  if (r < rows) fetch(r);
-  for (; r < rows; r += gridDim.x) {
-    V cx[VPT], cg[VPT];
-    const float m = nm, rs = nr;
-    float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      cx[j] = nx[j];
-      cg[j] = ng[j];
-      const bool in = tid + j * blockDim.x < vecs;
-#pragma unroll
-      for (int i = 0; i < VW; ++i) {
-        const float n = (to_f(cx[j].v[i]) - m) * rs, g = to_f(cg[j].v[i]);
-        const float gw = g * wr[j][i];
-        if (in) {
-          s[0] += gw;
-          s[1] = fmaf(gw, n, s[1]);
-          aw[j][i] = fmaf(g, n, aw[j][i]);
-          ab[j][i] += g;
-        }
-      }
-    }
-    if (r + gridDim.x < rows) fetch(r + gridDim.x);
-    if (!dx) continue;
-    block_sum<2>(s, red[flip], nw);
-    flip ^= 1;
-    const float c1 = s[0] * inv_d, c2 = s[1] * inv_d;
-    V* dst = reinterpret_cast<V*>(dx + r * d);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = tid + j * blockDim.x;
-      if (c < vecs) {
-        V o;
-#pragma unroll
-        for (int i = 0; i < VW; ++i) {
-          const float n = (to_f(cx[j].v[i]) - m) * rs;
-          o.v[i] = from_f<XT>(rs * (to_f(cg[j].v[i]) * wr[j][i] - c1 - n * c2));
-        }
-        dst[c] = o;
-      }
-    }
-  }
-  if (!part_w) return;
-  const int64_t base = (int64_t)blockIdx.x * d;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int c = tid + j * blockDim.x;
-    if (c < vecs)
-#pragma unroll
-      for (int i = 0; i < VW; ++i) {
-        part_w[base + c * VW + i] = aw[j][i];
-        part_b[base + c * VW + i] = ab[j][i];
-      }
-  }
-}
-
 // dw / db[c] = sum of the G per-block sums, in an order fixed by G: 32 slices
 // of blocks, each in order, then the slices in order.  Block = 32 columns.
 template <class WT>
@@ -606,6 +594,176 @@ __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__
     for (int i = 0; i < 32; ++i) s += slice ? sb[i][lane] : sw[i][lane];
     WT* out = slice ? db : dw;
     if (out) out[c] = from_f<WT>(s);
+  }
+}
+
+// ---------------------------------------------------------------- odd widths
+// Rows that do not start on 16-byte boundaries, many of them, forward: as
+// ln_fwd_rows_kernel, one element per access.
+constexpr int kOddElems = 32;                            // elements per lane
+constexpr int kOddWarps = 20;
+template <class XT>
+__global__ void __launch_bounds__(kOddWarps * 32, 1) ln_fwd_odd_kernel(const XT* __restrict__ x, const void* w,
+                                                                      const void* b, bool w_f32, int64_t rows, int d,
+                                                                      int wpr, float eps, XT* __restrict__ y,
+                                                                      float* __restrict__ mean,
+                                                                      float* __restrict__ rstd) {
+  extern __shared__ float2 wb2[];                        // [d]
+  __shared__ float red[2][kOddWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < d; i += kOddWarps * 32)
+    wb2[i] = make_float2(weight_at(w, w_f32, i), b ? weight_at(b, w_f32, i) : 0.0f);
+  __syncthreads();
+  const int group = warp / wpr, gw = warp - group * wpr, groups = kOddWarps / wpr;
+  const int tid = gw * 32 + lane, nt = wpr * 32;
+  const float inv_d = 1.0f / (float)d;
+  auto row_sum = [&](float s, float* buf) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (wpr > 1) {
+      if (lane == 0) buf[warp] = s;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(nt) : "memory");
+      s = 0.0f;
+      for (int i = 0; i < wpr; ++i) s += buf[group * wpr + i];
+    }
+    return s;
+  };
+  for (int64_t r = (int64_t)blockIdx.x * groups + group; r < rows; r += (int64_t)gridDim.x * groups) {
+    const XT* src = x + r * d;
+    float v[kOddElems], s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kOddElems; ++j) v[j] = tid + j * nt < d ? to_f(src[tid + j * nt]) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kOddElems; ++j) s += v[j];
+    const float m = row_sum(s, red[0]) * inv_d;
+    s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kOddElems; ++j) {
+      v[j] -= m;
+      if (tid + j * nt < d) s = fmaf(v[j], v[j], s);
+    }
+    const float rs = 1.0f / sqrtf(row_sum(s, red[1]) * inv_d + eps);
+#pragma unroll
+    for (int j = 0; j < kOddElems; ++j) {
+      const int c = tid + j * nt;
+      if (c < d) {
+        const float2 q = wb2[c];
+        y[r * d + c] = from_f<XT>(fmaf(v[j] * rs, q.x, q.y));
+      }
+    }
+    if (tid == 0) {
+      mean[r] = m;
+      rstd[r] = rs;
+    }
+  }
+}
+
+// Backward: as ln_bwd_rows_kernel, but rows are copied as the aligned 16-byte
+// chunks that cover them and read element by element, so threads read what
+// others copied: the step's barrier also publishes the next row.
+template <class XT, int EPT, int DEPTH>
+__global__ void __launch_bounds__(kMaxThreads, 1) ln_bwd_odd_kernel(
+    const XT* __restrict__ dy, const XT* __restrict__ x, const void* w, bool w_f32, const float* __restrict__ mean,
+    const float* __restrict__ rstd, int64_t rows, int d, XT* __restrict__ dx, float* __restrict__ part_w,
+    float* __restrict__ part_b) {
+  extern __shared__ uint4 ring[];                        // [DEPTH][2][chunks]
+  __shared__ float2 red[2][32];                          // warps the block does not have stay 0
+  __shared__ float2 stats[DEPTH];
+  pdl_release();
+  const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t row_bytes = (int64_t)d * sizeof(XT), all_bytes = rows * row_bytes;
+  const int chunks = (int)(row_bytes / 16) + 2;
+  const float inv_d = 1.0f / (float)d;
+  float wr[EPT], aw[EPT], ab[EPT], px[EPT], pg[EPT];
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const int c = tid + j * nt;
+    wr[j] = c < d ? weight_at(w, w_f32, c) : 0.0f;
+    aw[j] = ab[j] = 0.0f;
+  }
+  if (tid < 32) red[0][tid] = red[1][tid] = make_float2(0.0f, 0.0f);
+  const int mine = (int)((rows - blockIdx.x + gridDim.x - 1) / gridDim.x);    // rows blockIdx.x + k * gridDim.x
+  auto fetch = [&](int k) {
+    if (k < mine) {
+      const int64_t row = blockIdx.x + (int64_t)k * gridDim.x;
+      const int64_t at = row * row_bytes, start = at & ~int64_t(15);
+      const int n = (int)((at + row_bytes - start + 15) / 16);
+      uint4* slot = ring + (k % DEPTH) * 2 * chunks;
+      for (int c = tid; c < n; c += nt) {
+        const int64_t from = start + 16 * c;
+        const int bytes = (int)min((int64_t)16, all_bytes - from);           // the tensor ends inside its last chunk
+        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(slot + c);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                     "l"(reinterpret_cast<const char*>(x) + from), "r"(bytes)
+                     : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16 * chunks),
+                     "l"(reinterpret_cast<const char*>(dy) + from), "r"(bytes)
+                     : "memory");
+      }
+      if (tid < 2) cp_async4(reinterpret_cast<float*>(&stats[k % DEPTH]) + tid, (tid ? rstd : mean) + row);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int k = 0; k < DEPTH - 1; ++k) fetch(k);
+  asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
+  __syncthreads();
+  float rs0 = 0.0f;                                      // rstd of row k - 1
+  for (int k = 0; k <= mine; ++k) {
+    fetch(k + DEPTH - 1);                                // into row k - 1's slot
+    const int64_t row = blockIdx.x + (int64_t)k * gridDim.x;
+    if (dx && k > 0) {
+      const float* row_red = reinterpret_cast<const float*>(red[(k + 1) & 1]);
+      float tot = row_red[lane] + row_red[lane + 32];
+#pragma unroll
+      for (int o = 2; o < 32; o <<= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+      const float c1 = __shfl_sync(0xffffffffu, tot, 0) * inv_d;
+      const float c2 = __shfl_sync(0xffffffffu, tot, 1) * inv_d * rs0 * rs0;
+      XT* out = dx + (row - gridDim.x) * d;
+#pragma unroll
+      for (int j = 0; j < EPT; ++j)
+        if (tid + j * nt < d) out[tid + j * nt] = from_f<XT>(fmaf(-px[j], c2, pg[j] - c1));
+    }
+    if (k < mine) {
+      const float2 q = stats[k % DEPTH];
+      const float m = q.x, rs = q.y;
+      const uint4* slot = ring + (k % DEPTH) * 2 * chunks;
+      const int shift = (int)((row * row_bytes) & 15) / (int)sizeof(XT);
+      const XT* sx = reinterpret_cast<const XT*>(slot) + shift;
+      const XT* sg = reinterpret_cast<const XT*>(slot + chunks) + shift;
+      float t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < EPT; ++j) {
+        const int c = tid + j * nt;
+        if (c < d) {
+          const float xm = to_f(sx[c]) - m, g = to_f(sg[c]);
+          const float gr = g * rs, gw = gr * wr[j];
+          t0 += gw;
+          t1 = fmaf(gw, xm, t1);
+          aw[j] = fmaf(gr, xm, aw[j]);
+          ab[j] += g;
+          px[j] = xm;
+          pg[j] = gw;
+        }
+      }
+      rs0 = rs;
+      float e = (lane & 1) ? t1 : t0;
+      e += __shfl_xor_sync(0xffffffffu, (lane & 1) ? t0 : t1, 1);
+#pragma unroll
+      for (int o = 2; o < 32; o <<= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+      if (lane < 2) reinterpret_cast<float*>(&red[k & 1][warp])[lane] = e;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
+    __syncthreads();
+  }
+  if (!part_w) return;
+  const int64_t base = (int64_t)blockIdx.x * d;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const int c = tid + j * nt;
+    if (c < d) {
+      part_w[base + c] = aw[j];
+      part_b[base + c] = ab[j];
+    }
   }
 }
 
@@ -709,13 +867,14 @@ int current_sms() {
   return std::max(1, sms);
 }
 
-// The backward on 16-byte accesses: 16 elements per thread, or one access
-// where that would leave a block with less than two warps.
+// The backward: 16 elements per thread, or fewer where that would leave a
+// block with less than two warps.
 Shape bwd_shape(int64_t d, int esize) {
   Shape s = shape_of(d, esize);
-  if (s.vw == 1 || !s.reg) return s;
+  if (!s.reg) return s;
   const int64_t vecs = d / s.vw;
-  s.vpt = vecs < 128 ? 1 : kMaxElems / s.vw;
+  if (s.vw == 1) s.vpt = d <= 128 ? 4 : kMaxElems;
+  else s.vpt = vecs < 128 ? 1 : kMaxElems / s.vw;
   s.threads = (int)(((vecs + s.vpt - 1) / s.vpt + 31) / 32 * 32);
   return s;
 }
@@ -736,16 +895,9 @@ cudaError_t fwd_go(const void* x, const void* w, const void* b, int64_t rows, in
       (const XT*)x, (const WT*)w, (const WT*)b, rows, d, eps, (XT*)y, mean, rstd);
   return cudaGetLastError();
 }
-template <class XT, class WT, int VW, int VPT>
-cudaError_t bwd_go(const void* dy, const void* x, const void* w, const float* mean, const float* rstd, int64_t rows,
-                   int d, void* dx, float* pw, float* pb, const Shape& s, int64_t blocks, cudaStream_t st) {
-  ln_bwd_kernel<XT, WT, VW, VPT><<<(unsigned)blocks, s.threads, 0, st>>>(
-      (const XT*)dy, (const XT*)x, (const WT*)w, mean, rstd, rows, d, (XT*)dx, pw, pb);
-  return cudaGetLastError();
-}
-
 // Forward over many rows: the fewest warps per row (1, 2, 4) whose lanes hold
-// it in 28 vectors, and how many vectors that takes.  0 warps: not possible.
+// it in 16 vectors, and how many vectors that takes (28 vectors and half the warps:
+// 92 us against 84 at 16384 x 7168).  0 warps: not possible.
 struct RowPlan {
   int wpr, nv;
 };
@@ -754,7 +906,7 @@ RowPlan row_plan(int64_t d, int esize) {
   const int64_t vecs = d * esize / 16;
   for (int wpr = 1; wpr <= 4; wpr *= 2) {
     const int64_t nv = (vecs + 32 * wpr - 1) / (32 * wpr);
-    if (nv <= 28) return {wpr, (int)nv};
+    if (nv <= 16) return {wpr, (int)nv};
   }
   return {0, 0};
 }
@@ -766,6 +918,7 @@ cudaError_t fwd_rows_go(const void* x, const void* w, const void* b, bool w_f32,
   auto kernel = ln_fwd_rows_kernel<XT, NV>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  constexpr int kRowWarps = row_warps(NV);
   const int64_t groups = kRowWarps / wpr;
   kernel<<<(unsigned)std::min<int64_t>((rows + groups - 1) / groups, sms), kRowWarps * 32, smem, st>>>(
       (const uint4*)x, w, b, w_f32, rows, d, wpr, eps, (uint4*)y, mean, rstd);
@@ -796,6 +949,52 @@ cudaError_t bwd_rows_go(const void* dy, const void* x, const void* w, bool w_f32
   return bwd_depth_go<XT, VPT, 3>(dy, x, w, w_f32, mean, rstd, rows, d, dx, pw, pb, s, blocks, st);
 }
 
+template <class XT, int EPT, int DEPTH>
+cudaError_t bwd_odd_depth_go(const void* dy, const void* x, const void* w, bool w_f32, const float* mean,
+                             const float* rstd, int64_t rows, int d, void* dx, float* pw, float* pb, const Shape& s,
+                             int64_t blocks, cudaStream_t st) {
+  const int smem = DEPTH * 2 * (d * (int)sizeof(XT) / 16 + 2) * 16;
+  auto kernel = ln_bwd_odd_kernel<XT, EPT, DEPTH>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)blocks, s.threads, smem, st>>>((const XT*)dy, (const XT*)x, w, w_f32, mean, rstd, rows, d, (XT*)dx,
+                                                   pw, pb);
+  return cudaGetLastError();
+}
+template <class XT, int EPT>
+cudaError_t bwd_odd_go(const void* dy, const void* x, const void* w, bool w_f32, const float* mean, const float* rstd,
+                       int64_t rows, int d, void* dx, float* pw, float* pb, const Shape& s, int64_t blocks,
+                       cudaStream_t st) {
+  const int per_sm = std::max(1, std::min(8, 512 / s.threads));
+  const int fit = (220 << 10) / per_sm / (2 * (d * (int)sizeof(XT) / 16 + 2) * 16);
+  return fit >= 5 ? bwd_odd_depth_go<XT, EPT, 5>(dy, x, w, w_f32, mean, rstd, rows, d, dx, pw, pb, s, blocks, st)
+                  : bwd_odd_depth_go<XT, EPT, 3>(dy, x, w, w_f32, mean, rstd, rows, d, dx, pw, pb, s, blocks, st);
+}
+
+template <class XT>
+cudaError_t fwd_narrow_go(const void* x, const void* w, const void* b, bool w_f32, int64_t rows, int d, float eps,
+                          void* y, float* mean, float* rstd, int sms, cudaStream_t st) {
+  const int vecs = d * (int)sizeof(XT) / 16;
+  int G = 1;
+  while (G < vecs) G <<= 1;
+  const int64_t per_block = 16 * (32 / G) * kNarrowSets;
+  ln_fwd_narrow_kernel<XT><<<(unsigned)std::min<int64_t>((rows + per_block - 1) / per_block, 2 * sms), 512, 0, st>>>(
+      (const uint4*)x, w, b, w_f32, rows, d, G, eps, (uint4*)y, mean, rstd);
+  return cudaGetLastError();
+}
+
+template <class XT>
+cudaError_t fwd_odd_go(const void* x, const void* w, const void* b, bool w_f32, int64_t rows, int d, int wpr, float eps,
+                       void* y, float* mean, float* rstd, int sms, cudaStream_t st) {
+  auto kernel = ln_fwd_odd_kernel<XT>;
+  const int64_t groups = kOddWarps / wpr;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, d * 8);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)std::min<int64_t>((rows + groups - 1) / groups, sms), kOddWarps * 32, d * 8, st>>>(
+      (const XT*)x, w, b, w_f32, rows, d, wpr, eps, (XT*)y, mean, rstd);
+  return cudaGetLastError();
+}
+
 // Calls GO<XT, WT, VW, VPT>(args...) for the shape's access width and count.
 #define LN_SCALAR(GO, ...)                                                    \
   do {                                                                        \
@@ -821,13 +1020,18 @@ cudaError_t fwd_types(const void* x, const void* w, const void* b, int64_t rows,
   const Shape s = shape_of(d, sizeof(XT));
   const int sms = current_sms();
   const RowPlan p = row_plan(d, sizeof(XT));
-  // many rows: enough to give every SM's 12 warps work; few are split over a block each instead
-  if (p.wpr && rows * p.wpr >= (int64_t)sms * kRowWarps) {
+  if (p.wpr && d * (int64_t)sizeof(XT) <= 512 && rows >= 512)
+    return fwd_narrow_go<XT>(x, w, b, sizeof(WT) == 4, rows, (int)d, eps, y, mean, rstd, sms, st);
+  // many rows: enough to give 12 warps of every SM work; few are split over a block each instead
+  if (p.wpr && rows * p.wpr >= (int64_t)sms * 12) {
     const bool wf = sizeof(WT) == 4;
     if (p.nv <= 4) return fwd_rows_go<XT, 4>(x, w, b, wf, rows, (int)d, p.wpr, eps, y, mean, rstd, sms, st);
     if (p.nv <= 8) return fwd_rows_go<XT, 8>(x, w, b, wf, rows, (int)d, p.wpr, eps, y, mean, rstd, sms, st);
-    if (p.nv <= 16) return fwd_rows_go<XT, 16>(x, w, b, wf, rows, (int)d, p.wpr, eps, y, mean, rstd, sms, st);
-    return fwd_rows_go<XT, 28>(x, w, b, wf, rows, (int)d, p.wpr, eps, y, mean, rstd, sms, st);
+    return fwd_rows_go<XT, 16>(x, w, b, wf, rows, (int)d, p.wpr, eps, y, mean, rstd, sms, st);
+  }
+  if (!p.wpr && d <= 4 * 32 * kOddElems && rows >= (int64_t)sms * 12) {
+    const int wpr = d <= 32 * kOddElems ? 1 : d <= 64 * kOddElems ? 2 : 4;
+    return fwd_odd_go<XT>(x, w, b, sizeof(WT) == 4, rows, (int)d, wpr, eps, y, mean, rstd, sms, st);
   }
   if (s.reg) LN_DISPATCH(fwd_go, x, w, b, rows, (int)d, eps, y, mean, rstd, s, sms, st);
   ln_fwd_long_kernel<XT, WT><<<(unsigned)std::min<int64_t>(rows, 4 * sms), 512, 0, st>>>(
@@ -844,7 +1048,9 @@ cudaError_t bwd_rows(const void* dy, const void* x, const void* w, const float* 
     return s.vpt == 1 ? bwd_rows_go<XT, 1>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st)
                       : bwd_rows_go<XT, kWide>(dy, x, w, wf, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
   }
-  if (s.reg) LN_SCALAR(bwd_go, dy, x, w, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
+  if (s.reg)
+    return s.vpt == 4 ? bwd_odd_go<XT, 4>(dy, x, w, sizeof(WT) == 4, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st)
+                      : bwd_odd_go<XT, 16>(dy, x, w, sizeof(WT) == 4, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
   cudaError_t e = cudaSuccess;
   if (dx) {
     ln_bwd_long_kernel<XT, WT><<<(unsigned)std::min<int64_t>(rows, 4 * current_sms()), 512, 0, st>>>(

@@ -110,7 +110,11 @@ def test_layer_norm(train, rows, d, xt, wt):
 
 @pytest.mark.parametrize("rows,d,xt", [(1824, 256, torch.bfloat16), (1900, 1024, torch.float32),
                                        (1825, 2056, torch.bfloat16), (1830, 7168, torch.bfloat16),
-                                       (930, 7168, torch.float32), (2001, 72, torch.bfloat16)])
+                                       (930, 7168, torch.float32), (2001, 72, torch.bfloat16),
+                                       (1999, 1001, torch.float32), (1830, 1003, torch.bfloat16),
+                                       (1900, 2051, torch.float32), (2000, 4099, torch.bfloat16),
+                                       (1850, 13, torch.bfloat16), (700, 8, torch.bfloat16), (513, 128, torch.float32),
+                                       (3000, 200, torch.bfloat16), (10007, 64, torch.bfloat16)])
 def test_layer_norm_many_rows(train, rows, d, xt):
     check_ln(train, *ln_inputs(rows, d, xt, torch.float32, seed=7))
 
