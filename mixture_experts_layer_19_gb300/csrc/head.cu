@@ -100,6 +100,7 @@ struct Layout {
   int64_t Tp, piece, ldl;   // padded rows, columns of one piece, leading dimension of the D piece
   int K, nsplit;
   bool pair_z, pair_x, pair_w;   // CTA pairs for the logits, dX and dW products
+  int arows;                // rows of A per CTA in the logits products
   bool sums;                // dX needs the fp32 sums (several pieces or splits)
   int64_t blocks;           // blocks of 128 vocabulary columns
   size_t counts, scale, rec, inv, ids, probs, first, cnt, plogp, xc, part, zt, dl, acc, total;
@@ -154,6 +155,7 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
   }
   L.pair_z = better_as_pair(c.T, backward ? std::min<int64_t>(L.piece, c.V) : c.V, (double)ceil_div(c.d, 64),
                             kEpiLogits, sms, pairs);
+  L.arows = L.pair_z || c.T > 64 ? 128 : c.T > 16 ? 64 : 16;
   size_t o = 0;
   auto take = [&o](size_t bytes) {
     const size_t at = o;
@@ -289,7 +291,7 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   a.out_scale = temp;
   a.stall = (c.debug_flags & MOE_DEBUG_STALL_TEST) ? 1 : 0;
 
-  bool ok = map_k(&a.mapA0, h.X, c.d, T, c.d, 128) && map_k(&a.mapA1, r.Xc, c.d, L.Tp, c.d, 128) &&
+  bool ok = map_k(&a.mapA0, h.X, c.d, T, c.d, L.arows) && map_k(&a.mapA1, r.Xc, c.d, L.Tp, c.d, L.arows) &&
             map_k(&a.mapB0, h.W, c.d, c.V, c.d, L.pair_z ? 128 : 256);
   HeadArgs ax{}, aw{};
   if (backward) {
@@ -318,7 +320,7 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   auto go = [&](int kind, bool pair, const HeadArgs& args, int64_t m, int64_t ncols, int splits) {
     const int64_t tiles = ceil_div(m, pair ? 256 : 128) * ceil_div(ncols, kHeadBN) * splits;
     const int64_t workers = std::min<int64_t>(tiles, pair ? f.pairs : f.sms);
-    return head_gemm_launch(kind, pair, args, (int)workers * (pair ? 2 : 1), h.st);
+    return head_gemm_launch(kind, pair, L.arows, args, (int)workers * (pair ? 2 : 1), h.st);
   };
   if (!backward) {
     a.v0 = 0;

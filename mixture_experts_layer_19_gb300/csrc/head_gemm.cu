@@ -5,51 +5,63 @@ namespace moe {
 
 namespace {
 
-template <int KIND, int CG, bool TEACHER>
+template <int KIND, int CG, bool TEACHER, int AR = kHBM>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(head_gemm_kernel<KIND, CG, TEACHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              HeadTraits<KIND, CG>::smem_bytes);
+  return cudaFuncSetAttribute(head_gemm_kernel<KIND, CG, TEACHER, AR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              HeadTraits<KIND, CG, AR>::smem_bytes);
 }
 
-template <int KIND, int CG, bool TEACHER>
+template <int KIND, int CG, bool TEACHER, int AR = kHBM>
 cudaError_t launch_one(const HeadArgs& a, int grid, cudaStream_t st) {
-  return launch_pdl(head_gemm_kernel<KIND, CG, TEACHER>, dim3(grid), dim3(kHeadThreads), HeadTraits<KIND, CG>::smem_bytes, st,
+  return launch_pdl(head_gemm_kernel<KIND, CG, TEACHER, AR>, dim3(grid), dim3(kHeadThreads), HeadTraits<KIND, CG, AR>::smem_bytes, st,
                     CG, a);
 }
 
-template <int CG>
-cudaError_t launch_kind(int kind, const HeadArgs& a, int grid, cudaStream_t st) {
-  const bool teacher = a.first != nullptr;
-  switch (kind) {
-    case kHeadLse:
-      return teacher ? launch_one<kHeadLse, CG, true>(a, grid, st) : launch_one<kHeadLse, CG, false>(a, grid, st);
-    case kHeadDl:
-      return teacher ? launch_one<kHeadDl, CG, true>(a, grid, st) : launch_one<kHeadDl, CG, false>(a, grid, st);
-    case kHeadDX: return launch_one<kHeadDX, CG, false>(a, grid, st);
-    default: return launch_one<kHeadDW, CG, false>(a, grid, st);
-  }
+template <int KIND, int CG, int AR>
+cudaError_t launch_targets(const HeadArgs& a, int grid, cudaStream_t st) {
+  return a.first ? launch_one<KIND, CG, true, AR>(a, grid, st) : launch_one<KIND, CG, false, AR>(a, grid, st);
 }
 
-template <int CG>
-cudaError_t prepare_kinds() {
-  cudaError_t e = prepare_one<kHeadLse, CG, false>();
-  if (e == cudaSuccess) e = prepare_one<kHeadLse, CG, true>();
-  if (e == cudaSuccess) e = prepare_one<kHeadDl, CG, false>();
-  if (e == cudaSuccess) e = prepare_one<kHeadDl, CG, true>();
-  if (e == cudaSuccess) e = prepare_one<kHeadDX, CG, false>();
-  if (e == cudaSuccess) e = prepare_one<kHeadDW, CG, false>();
+template <int KIND>
+cudaError_t launch_logits(bool pair, int arows, const HeadArgs& a, int grid, cudaStream_t st) {
+  if (pair) return launch_targets<KIND, 2, kHBM>(a, grid, st);
+  if (arows == 16) return launch_targets<KIND, 1, 16>(a, grid, st);
+  if (arows == 64) return launch_targets<KIND, 1, 64>(a, grid, st);
+  return launch_targets<KIND, 1, kHBM>(a, grid, st);
+}
+
+template <int KIND>
+cudaError_t prepare_logits() {
+  cudaError_t e = prepare_one<KIND, 2, false>();
+  if (e == cudaSuccess) e = prepare_one<KIND, 2, true>();
+  if (e == cudaSuccess) e = prepare_one<KIND, 1, false>();
+  if (e == cudaSuccess) e = prepare_one<KIND, 1, true>();
+  if (e == cudaSuccess) e = prepare_one<KIND, 1, false, 16>();
+  if (e == cudaSuccess) e = prepare_one<KIND, 1, true, 16>();
+  if (e == cudaSuccess) e = prepare_one<KIND, 1, false, 64>();
+  if (e == cudaSuccess) e = prepare_one<KIND, 1, true, 64>();
   return e;
 }
 
 }  // namespace
 
 cudaError_t head_gemm_prepare() {
-  cudaError_t e = prepare_kinds<1>();
-  return e == cudaSuccess ? prepare_kinds<2>() : e;
+  cudaError_t e = prepare_logits<kHeadLse>();
+  if (e == cudaSuccess) e = prepare_logits<kHeadDl>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDX, 1, false>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDX, 2, false>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDW, 1, false>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDW, 2, false>();
+  return e;
 }
 
-cudaError_t head_gemm_launch(int kind, bool pair, const HeadArgs& a, int grid, cudaStream_t st) {
-  return pair ? launch_kind<2>(kind, a, grid, st) : launch_kind<1>(kind, a, grid, st);
+cudaError_t head_gemm_launch(int kind, bool pair, int arows, const HeadArgs& a, int grid, cudaStream_t st) {
+  switch (kind) {
+    case kHeadLse: return launch_logits<kHeadLse>(pair, arows, a, grid, st);
+    case kHeadDl: return launch_logits<kHeadDl>(pair, arows, a, grid, st);
+    case kHeadDX: return pair ? launch_one<kHeadDX, 2, false>(a, grid, st) : launch_one<kHeadDX, 1, false>(a, grid, st);
+    default: return pair ? launch_one<kHeadDW, 2, false>(a, grid, st) : launch_one<kHeadDW, 1, false>(a, grid, st);
+  }
 }
 
 // How many CTA pairs the device holds at once: the static schedule's grid.
@@ -57,7 +69,7 @@ cudaError_t head_gemm_max_pairs(int* pairs) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kHeadThreads);
-  cfg.dynamicSmemBytes = HeadTraits<kHeadDl, 2>::smem_bytes;
+  cfg.dynamicSmemBytes = HeadTraits<kHeadDl, 2, kHBM>::smem_bytes;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -65,7 +77,7 @@ cudaError_t head_gemm_max_pairs(int* pairs) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(pairs, head_gemm_kernel<kHeadDl, 2, false>, &cfg);
+  return cudaOccupancyMaxActiveClusters(pairs, head_gemm_kernel<kHeadDl, 2, false, kHBM>, &cfg);
 }
 
 }  // namespace moe

@@ -36,18 +36,24 @@ constexpr int kHeadThreads = 320;
 constexpr int kHeadEpiWarps = 8;
 constexpr int kLseChunk = 16;                // K slices per accumulator of kHeadLse (1024)
 
-template <int KIND, int CG>
+// AR rows of A are fetched per CTA: 128, or 16 or 64 when the call has no more
+// tokens.  The product still covers 128 rows -- those past AR read whatever
+// follows in shared memory, and no one reads their results -- but the stages get
+// smaller, and more of W is on its way, which is what a call of few tokens waits for.
+template <int KIND, int CG, int AR>
 struct HeadTraits {
+  static_assert(AR == kHBM || (CG == 1 && KIND <= kHeadDl));
   static constexpr bool a_mn = KIND == kHeadDW;
   static constexpr bool b_mn = KIND == kHeadDX || KIND == kHeadDW;
-  static constexpr int a_bytes = kHBM * kHBK * 2;             // 16 KB
+  static constexpr int a_bytes = AR * kHBK * 2;               // 16 KB for 128 rows
   static constexpr int b_rows = kHeadBN / CG;
   static constexpr int b_bytes = b_rows * kHBK * 2;           // 32 / 16 KB
   static constexpr int stage_bytes = a_bytes + b_bytes;
-  static constexpr int stages = CG == 2 ? 6 : 4;
   // staging per epilogue warp: 32 rows of 128 bytes
   static constexpr int staging = KIND == kHeadLse ? 0 : 4096;
-  static constexpr int smem_bytes = stages * stage_bytes + kHeadEpiWarps * staging + 1024 + 256;
+  static constexpr int spare = kHeadEpiWarps * staging + 1024 + 256;
+  static constexpr int stages = AR == kHBM ? (CG == 2 ? 6 : 4) : (232448 - spare) / stage_bytes;
+  static constexpr int smem_bytes = stages * stage_bytes + spare;
 };
 
 struct HeadTile {
@@ -256,9 +262,9 @@ __device__ __forceinline__ float pick32(const float* v, int col) {
   return (col & 16) ? t[2] : t[0];
 }
 
-template <int KIND, int CG, bool TEACHER>
+template <int KIND, int CG, bool TEACHER, int AR>
 __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid_constant__ HeadArgs g) {
-  using TR = HeadTraits<KIND, CG>;
+  using TR = HeadTraits<KIND, CG, AR>;
   constexpr int kSt = TR::stages;
   extern __shared__ uint8_t smem_raw[];
   // every CTA of a launch has the same dynamic shared-memory base, so a pair's layouts coincide

@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(row_warps(NV) * 32, 1) ln_fwd_rows_kernel(cons
 // Narrow rows (at most 32 vectors): G lanes per row, 32 / G rows side by side
 // in a warp and four such sets in flight; the weights stay in registers.  One
 // row at a time leaves too few bytes in flight: 46.7 us at 131072 x 256
-// against XX.
+// against 31.9.
 constexpr int kNarrowSets = 4;
 template <class XT>
 __global__ void __launch_bounds__(512, 2) ln_fwd_narrow_kernel(const uint4* __restrict__ x, const void* w,
