@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
       // ------------------------------------------------------------ producer
       fence_proxy_async_global();                       // the predecessors' plain stores, read by TMA below
       const uint64_t pol = policy_evict_last();
+      const uint64_t pol_b = KIND == kHeadLse && g.T <= kHBM * CG ? policy_evict_first() : pol;
       const bool all = na == g.T;                       // no row skipped: X is read in place
       const CUtensorMap* mA = (KIND <= kHeadDl && !all) ? &g.mapA1 : &g.mapA0;
       const CUtensorMap* mB = (KIND == kHeadDW && !all) ? &g.mapB1 : &g.mapB0;
@@ -341,22 +342,22 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           uint8_t* sb = sa + TR::a_bytes;
           const int32_t k0 = (t.kb0 + kb) * kHBK;
           const uint32_t bar_c = CG == 2 ? mapa_u32(smem_u32(&full[s]), 0) : 0;
-          auto load = [&](uint8_t* dst, const CUtensorMap* m, int64_t x, int64_t y) {
+          auto load = [&](uint8_t* dst, const CUtensorMap* m, int64_t x, int64_t y, uint64_t pol) {
             if constexpr (CG == 1) tma_load_2d(dst, m, (int32_t)x, (int32_t)y, &full[s], pol);
             else tma_load_2d_pair(dst, m, (int32_t)x, (int32_t)y, bar_c, pol);
           };
           if (KIND == kHeadDW) {
 #pragma unroll
-            for (int j = 0; j < kHBM / 64; ++j) load(sa + j * 8192, mA, arow + j * 64, k0);
+            for (int j = 0; j < kHBM / 64; ++j) load(sa + j * 8192, mA, arow + j * 64, k0, pol);
           } else {
-            load(sa, mA, k0, arow);
+            load(sa, mA, k0, arow, pol);
           }
           if (KIND == kHeadDX || KIND == kHeadDW) {
             const int64_t krow = (KIND == kHeadDX ? g.v0 : 0) + k0;
 #pragma unroll
-            for (int j = 0; j < TR::b_rows / 64; ++j) load(sb + j * 8192, mB, bcol + j * 64, krow);
+            for (int j = 0; j < TR::b_rows / 64; ++j) load(sb + j * 8192, mB, bcol + j * 64, krow, pol_b);
           } else {
-            load(sb, mB, k0, g.v0 + bcol);
+            load(sb, mB, k0, g.v0 + bcol, pol_b);
           }
           issued |= 1u << s;
           last_par = (last_par & ~(1u << s)) | (ph << s);
