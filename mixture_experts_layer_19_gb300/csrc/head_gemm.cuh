@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
       // ------------------------------------------------------------ producer
       fence_proxy_async_global();                       // the predecessors' plain stores, read by TMA below
       const uint64_t pol = policy_evict_last();
-      const uint64_t pol_b = KIND == kHeadLse && g.T <= kHBM * CG ? policy_evict_first() : pol;
+      const uint64_t pol_b = (KIND == kHeadLse || KIND == kHeadDX) && g.T <= kHBM * CG ? policy_evict_first() : pol;
       const bool all = na == g.T;                       // no row skipped: X is read in place
       const CUtensorMap* mA = (KIND <= kHeadDl && !all) ? &g.mapA1 : &g.mapA0;
       const CUtensorMap* mB = (KIND == kHeadDW && !all) ? &g.mapB1 : &g.mapB0;
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
               if (to >= 0 && x < g.d) *reinterpret_cast<uint4*>(g.dX + (int64_t)to * g.d + x) = u;
             } else {
               if (rowq + rr < g.vlen && x < g.d)
-                *reinterpret_cast<uint4*>(g.dW + (g.v0 + rowq + rr) * g.d + x) = u;
+                __stcs(reinterpret_cast<uint4*>(g.dW + (g.v0 + rowq + rr) * g.d + x), u);
             }
           }
           __syncwarp();
