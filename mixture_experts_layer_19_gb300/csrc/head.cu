@@ -135,12 +135,13 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
     L.ldl = L.piece;
     const int64_t cols = std::min<int64_t>(L.piece, c.V);
     // dX has few tiles when T is small: its K, the piece, is split until they
-    // fill the SMs; a split costs the traffic of its fp32 sums (about 2 slices)
+    // fill the SMs.  Splitting costs another launch (12 slices) and each split
+    // the traffic of its fp32 sums (about 2)
     const int64_t nkb = ceil_div(cols, 64);
     double best = 0;
     for (int pair = 0; pair < 2; ++pair)
       for (int s = 1; s <= 16 && s <= nkb; ++s) {
-        const double cost = tiles_cost(c.T, c.d, (double)nkb / s, kEpiGrad, s, pair != 0, sms, pairs) + 2.0 * (s - 1);
+        const double cost = tiles_cost(c.T, c.d, (double)nkb / s, kEpiGrad, s, pair != 0, sms, pairs) + (s > 1 ? 12.0 + 2.0 * (s - 1) : 0.0);
         if ((s == 1 && !pair) || cost < best) {
           best = cost;
           L.nsplit = s;
@@ -303,6 +304,7 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
     ok = ok && map_k(&ax.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 128) && map_k(&ax.mapB0, h.W, c.d, c.V, c.d, 64);
     aw = a;
     aw.dW = static_cast<__nv_bfloat16*>(h.dW);
+    aw.beside = h.dX != nullptr;
     ok = ok && map_k(&aw.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 64) && map_k(&aw.mapB0, h.X, c.d, T, c.d, 64) &&
          map_k(&aw.mapB1, r.Xc, c.d, L.Tp, c.d, 64);
   }

@@ -49,6 +49,7 @@ struct HeadArgs {
   int add;                   // kHeadDX: add into the fp32 sums (0: first piece, overwrite)
   float inv_temp;            // 1 / temperature
   float out_scale;           // temperature, multiplied with *scale
+  int beside;                // kHeadDW: the launch before is this call's dX
   int stall;                 // test hook: the producer issues nothing
 };
 

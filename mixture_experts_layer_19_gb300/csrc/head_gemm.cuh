@@ -310,8 +310,14 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
   if constexpr (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait();
-  pdl_release();
+  // dW behind dX reads nothing that dX writes, and dX let it start only after
+  // everything earlier was complete: the two overlap, and dW waits at its end,
+  // so that whatever follows finds both complete.
+  const bool beside = KIND == kHeadDW && g.beside;
+  if (!beside) {
+    pdl_wait();
+    pdl_release();
+  }
   WaitCtl wc{g.status, abort_flag, g.timeout_ns};
 
   const int na = *g.n_active;
@@ -673,6 +679,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     tc_fence_after();
     head_tmem_free<CG>(tmem_base);
   }
+  if (beside) pdl_wait();
 }
 
 }  // namespace moe
