@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_kernel(const XT* __restric
                                                              const WT* __restrict__ b, int64_t rows, int d, float eps,
                                                              XT* __restrict__ y, float* __restrict__ mean,
                                                              float* __restrict__ rstd) {
+  pdl_wait();
+  pdl_release();
   using V = Vec<XT, VW>;
   __shared__ float red[2][16][1];
   const int vecs = d / VW, nw = blockDim.x >> 5, tid = threadIdx.x;
@@ -253,6 +255,8 @@ __global__ void __launch_bounds__(row_warps(NV) * 32, 1) ln_fwd_rows_kernel(cons
                                                                        int wpr, float eps, uint4* __restrict__ y,
                                                                        float* __restrict__ mean,
                                                                        float* __restrict__ rstd) {
+  pdl_wait();
+  pdl_release();
   using P = Pairs<XT>;
   constexpr int kRowWarps = row_warps(NV);
   extern __shared__ float4 wb[];                         // [P::n][vecs]
@@ -345,6 +349,8 @@ __global__ void __launch_bounds__(512, 2) ln_fwd_narrow_kernel(const uint4* __re
                                                                const void* b, bool w_f32, int64_t rows, int d, int G,
                                                                float eps, uint4* __restrict__ y,
                                                                float* __restrict__ mean, float* __restrict__ rstd) {
+  pdl_wait();
+  pdl_release();
   using P = Pairs<XT>;
   const int vecs = d / (2 * P::n), lane = threadIdx.x & 31;
   const int c = lane & (G - 1), per = 32 / G;
@@ -435,11 +441,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) ln_bwd_rows_kernel(
     const uint4* __restrict__ dy, const uint4* __restrict__ x, const void* w, bool w_f32,
     const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows, int d,
     uint4* __restrict__ dx, float* __restrict__ part_w, float* __restrict__ part_b) {
+  pdl_wait();
+  pdl_release();
   using P = Pairs<XT>;
   extern __shared__ uint4 ring[];                        // [DEPTH][2][VPT * threads]
   __shared__ float2 red[2][32];                          // warps the block does not have stay 0
   __shared__ float2 stats[DEPTH][32];                    // (mean, rstd) of a row, copied by each warp for itself
-  pdl_release();
   const int vecs = d / (2 * P::n), tid = threadIdx.x, nt = blockDim.x;
   if (tid < 32) red[0][tid] = red[1][tid] = make_float2(0.0f, 0.0f);
   __syncthreads();
@@ -451,10 +458,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) ln_bwd_rows_kernel(
   for (int j = 0; j < VPT; ++j) {
     const int c = tid + j * nt;
     in[j] = c < vecs;
+    float wv[2 * P::n] = {};
+    if (in[j]) {
+      if (w_f32) load_weights<float, 2 * P::n>(reinterpret_cast<const float*>(w) + c * 2 * P::n, wv);
+      else load_weights<__nv_bfloat16, 2 * P::n>(reinterpret_cast<const __nv_bfloat16*>(w) + c * 2 * P::n, wv);
+    }
 #pragma unroll
     for (int p = 0; p < P::n; ++p) {
-      const int e = c * 2 * P::n + 2 * p;
-      wr[j][p] = in[j] ? f2_make(weight_at(w, w_f32, e), weight_at(w, w_f32, e + 1)) : f2_make(0, 0);
+      wr[j][p] = f2_make(wv[2 * p], wv[2 * p + 1]);
       aw[j][p] = ab[j][p] = f2_make(0, 0);
     }
     // slots of columns past the row stay zero: they add nothing
@@ -576,12 +587,14 @@ template <class WT>
 __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__ part_w,
                                                        const float* __restrict__ part_b, int G, int d,
                                                        WT* __restrict__ dw, WT* __restrict__ db) {
-  __shared__ float sw[32][33], sb[32][33];
   pdl_wait();
+  pdl_release();
+  __shared__ float sw[32][33], sb[32][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.0f, b = 0.0f;
   if (c < d)
+#pragma unroll 8
     for (int g = slice; g < G; g += 32) {
       a += part_w[(int64_t)g * d + c];
       b += part_b[(int64_t)g * d + c];
@@ -608,6 +621,8 @@ __global__ void __launch_bounds__(kOddWarps * 32, 1) ln_fwd_odd_kernel(const XT*
                                                                       int wpr, float eps, XT* __restrict__ y,
                                                                       float* __restrict__ mean,
                                                                       float* __restrict__ rstd) {
+  pdl_wait();
+  pdl_release();
   extern __shared__ float2 wb2[];                        // [d]
   __shared__ float red[2][kOddWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -666,10 +681,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) ln_bwd_odd_kernel(
     const XT* __restrict__ dy, const XT* __restrict__ x, const void* w, bool w_f32, const float* __restrict__ mean,
     const float* __restrict__ rstd, int64_t rows, int d, XT* __restrict__ dx, float* __restrict__ part_w,
     float* __restrict__ part_b) {
+  pdl_wait();
+  pdl_release();
   extern __shared__ uint4 ring[];                        // [DEPTH][2][chunks]
   __shared__ float2 red[2][32];                          // warps the block does not have stay 0
   __shared__ float2 stats[DEPTH];
-  pdl_release();
   const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row_bytes = (int64_t)d * sizeof(XT), all_bytes = rows * row_bytes;
   const int chunks = (int)(row_bytes / 16) + 2;
@@ -773,6 +789,8 @@ __global__ void __launch_bounds__(512) ln_fwd_long_kernel(const XT* __restrict__
                                                           const WT* __restrict__ b, int64_t rows, int64_t d, float eps,
                                                           XT* __restrict__ y, float* __restrict__ mean,
                                                           float* __restrict__ rstd) {
+  pdl_wait();
+  pdl_release();
   __shared__ float red[2][16][1];
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const XT* src = x + r * d;
@@ -800,6 +818,8 @@ __global__ void __launch_bounds__(512) ln_bwd_long_kernel(const XT* __restrict__
                                                           const WT* __restrict__ w, const float* __restrict__ mean,
                                                           const float* __restrict__ rstd, int64_t rows, int64_t d,
                                                           XT* __restrict__ dx) {
+  pdl_wait();
+  pdl_release();
   __shared__ float red[2][16][2];
   int flip = 0;
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -825,6 +845,8 @@ __global__ void __launch_bounds__(256) ln_bwd_long_cols_kernel(const XT* __restr
                                                                const float* __restrict__ mean,
                                                                const float* __restrict__ rstd, int64_t rows, int64_t d,
                                                                float* __restrict__ part_w, float* __restrict__ part_b) {
+  pdl_wait();
+  pdl_release();
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= d) return;
   const int64_t lo = rows * blockIdx.y / gridDim.y, hi = rows * (blockIdx.y + 1) / gridDim.y;
@@ -891,9 +913,8 @@ int64_t long_slices(int64_t rows) { return std::min<int64_t>(rows, 32); }
 template <class XT, class WT, int VW, int VPT>
 cudaError_t fwd_go(const void* x, const void* w, const void* b, int64_t rows, int d, float eps, void* y, float* mean,
                    float* rstd, const Shape& s, int sms, cudaStream_t st) {
-  ln_fwd_kernel<XT, WT, VW, VPT><<<(unsigned)fwd_blocks(rows, s, sms), s.threads, 0, st>>>(
-      (const XT*)x, (const WT*)w, (const WT*)b, rows, d, eps, (XT*)y, mean, rstd);
-  return cudaGetLastError();
+  return launch_pdl(ln_fwd_kernel<XT, WT, VW, VPT>, dim3((unsigned)fwd_blocks(rows, s, sms)), dim3(s.threads), 0, st, 1,
+                    (const XT*)x, (const WT*)w, (const WT*)b, rows, d, eps, (XT*)y, mean, rstd);
 }
 // Forward over many rows: the fewest warps per row (1, 2, 4) whose lanes hold
 // it in 16 vectors, and how many vectors that takes (28 vectors and half the warps:
@@ -920,9 +941,8 @@ cudaError_t fwd_rows_go(const void* x, const void* w, const void* b, bool w_f32,
   if (e != cudaSuccess) return e;
   constexpr int kRowWarps = row_warps(NV);
   const int64_t groups = kRowWarps / wpr;
-  kernel<<<(unsigned)std::min<int64_t>((rows + groups - 1) / groups, sms), kRowWarps * 32, smem, st>>>(
-      (const uint4*)x, w, b, w_f32, rows, d, wpr, eps, (uint4*)y, mean, rstd);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>((rows + groups - 1) / groups, sms)), dim3(kRowWarps * 32),
+                    smem, st, 1, (const uint4*)x, w, b, w_f32, rows, d, wpr, eps, (uint4*)y, mean, rstd);
 }
 
 template <class XT, int VPT, int DEPTH>
@@ -933,9 +953,8 @@ cudaError_t bwd_depth_go(const void* dy, const void* x, const void* w, bool w_f3
   auto kernel = ln_bwd_rows_kernel<XT, VPT, DEPTH>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)blocks, s.threads, smem, st>>>((const uint4*)dy, (const uint4*)x, w, w_f32, mean, rstd, rows, d,
-                                                   (uint4*)dx, pw, pb);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(s.threads), smem, st, 1, (const uint4*)dy, (const uint4*)x, w,
+                    w_f32, mean, rstd, rows, d, (uint4*)dx, pw, pb);
 }
 // As many rows in flight as shared memory has room for, up to 7.
 template <class XT, int VPT>
@@ -957,9 +976,8 @@ cudaError_t bwd_odd_depth_go(const void* dy, const void* x, const void* w, bool 
   auto kernel = ln_bwd_odd_kernel<XT, EPT, DEPTH>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)blocks, s.threads, smem, st>>>((const XT*)dy, (const XT*)x, w, w_f32, mean, rstd, rows, d, (XT*)dx,
-                                                   pw, pb);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(s.threads), smem, st, 1, (const XT*)dy, (const XT*)x, w, w_f32,
+                    mean, rstd, rows, d, (XT*)dx, pw, pb);
 }
 template <class XT, int EPT>
 cudaError_t bwd_odd_go(const void* dy, const void* x, const void* w, bool w_f32, const float* mean, const float* rstd,
@@ -978,9 +996,9 @@ cudaError_t fwd_narrow_go(const void* x, const void* w, const void* b, bool w_f3
   int G = 1;
   while (G < vecs) G <<= 1;
   const int64_t per_block = 16 * (32 / G) * kNarrowSets;
-  ln_fwd_narrow_kernel<XT><<<(unsigned)std::min<int64_t>((rows + per_block - 1) / per_block, 2 * sms), 512, 0, st>>>(
-      (const uint4*)x, w, b, w_f32, rows, d, G, eps, (uint4*)y, mean, rstd);
-  return cudaGetLastError();
+  return launch_pdl(ln_fwd_narrow_kernel<XT>,
+                    dim3((unsigned)std::min<int64_t>((rows + per_block - 1) / per_block, 2 * sms)), dim3(512), 0, st, 1,
+                    (const uint4*)x, w, b, w_f32, rows, d, G, eps, (uint4*)y, mean, rstd);
 }
 
 template <class XT>
@@ -990,9 +1008,8 @@ cudaError_t fwd_odd_go(const void* x, const void* w, const void* b, bool w_f32, 
   const int64_t groups = kOddWarps / wpr;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, d * 8);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)std::min<int64_t>((rows + groups - 1) / groups, sms), kOddWarps * 32, d * 8, st>>>(
-      (const XT*)x, w, b, w_f32, rows, d, wpr, eps, (XT*)y, mean, rstd);
-  return cudaGetLastError();
+  return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>((rows + groups - 1) / groups, sms)), dim3(kOddWarps * 32),
+                    d * 8, st, 1, (const XT*)x, w, b, w_f32, rows, d, wpr, eps, (XT*)y, mean, rstd);
 }
 
 // Calls GO<XT, WT, VW, VPT>(args...) for the shape's access width and count.
@@ -1034,9 +1051,8 @@ cudaError_t fwd_types(const void* x, const void* w, const void* b, int64_t rows,
     return fwd_odd_go<XT>(x, w, b, sizeof(WT) == 4, rows, (int)d, wpr, eps, y, mean, rstd, sms, st);
   }
   if (s.reg) LN_DISPATCH(fwd_go, x, w, b, rows, (int)d, eps, y, mean, rstd, s, sms, st);
-  ln_fwd_long_kernel<XT, WT><<<(unsigned)std::min<int64_t>(rows, 4 * sms), 512, 0, st>>>(
-      (const XT*)x, (const WT*)w, (const WT*)b, rows, d, eps, (XT*)y, mean, rstd);
-  return cudaGetLastError();
+  return launch_pdl(ln_fwd_long_kernel<XT, WT>, dim3((unsigned)std::min<int64_t>(rows, 4 * sms)), dim3(512), 0, st, 1,
+                    (const XT*)x, (const WT*)w, (const WT*)b, rows, d, eps, (XT*)y, mean, rstd);
 }
 
 template <class XT, class WT>
@@ -1053,14 +1069,12 @@ cudaError_t bwd_rows(const void* dy, const void* x, const void* w, const float* 
                       : bwd_odd_go<XT, 16>(dy, x, w, sizeof(WT) == 4, mean, rstd, rows, (int)d, dx, pw, pb, s, blocks, st);
   cudaError_t e = cudaSuccess;
   if (dx) {
-    ln_bwd_long_kernel<XT, WT><<<(unsigned)std::min<int64_t>(rows, 4 * current_sms()), 512, 0, st>>>(
-        (const XT*)dy, (const XT*)x, (const WT*)w, mean, rstd, rows, d, (XT*)dx);
-    e = cudaGetLastError();
+    e = launch_pdl(ln_bwd_long_kernel<XT, WT>, dim3((unsigned)std::min<int64_t>(rows, 4 * current_sms())), dim3(512), 0,
+                   st, 1, (const XT*)dy, (const XT*)x, (const WT*)w, mean, rstd, rows, d, (XT*)dx);
   }
   if (e == cudaSuccess && pw) {
-    ln_bwd_long_cols_kernel<XT><<<dim3((unsigned)((d + 255) / 256), (unsigned)blocks), 256, 0, st>>>(
-        (const XT*)dy, (const XT*)x, mean, rstd, rows, d, pw, pb);
-    e = cudaGetLastError();
+    e = launch_pdl(ln_bwd_long_cols_kernel<XT>, dim3((unsigned)((d + 255) / 256), (unsigned)blocks), dim3(256), 0, st, 1,
+                   (const XT*)dy, (const XT*)x, mean, rstd, rows, d, pw, pb);
   }
   return e;
 }
