@@ -141,7 +141,8 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
     double best = 0;
     for (int pair = 0; pair < 2; ++pair)
       for (int s = 1; s <= 16 && s <= nkb; ++s) {
-        const double cost = tiles_cost(c.T, c.d, (double)nkb / s, kEpiGrad, s, pair != 0, sms, pairs) + (s > 1 ? 12.0 + 2.0 * (s - 1) : 0.0);
+        const double cost = tiles_cost(c.T, c.d, (double)nkb / s, kEpiGrad, s, pair != 0, sms, pairs) +
+                            (s > 1 ? 12.0 + 2.0 * (s - 1) : 0.0);
         if ((s == 1 && !pair) || cost < best) {
           best = cost;
           L.nsplit = s;
@@ -283,7 +284,6 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   a.status = h.status;
   a.timeout_ns = c.wait_timeout_ns > 0 ? (uint64_t)c.wait_timeout_ns : 2000000000ull;
   a.Tp = L.Tp;
-  a.V = c.V;
   a.T = T;
   a.d = c.d;
   a.K = L.K;
@@ -315,8 +315,8 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   if (distill)
     e = launch_head_entries(h.teacher, c.teacher_bf16 != 0, h.ids, c.ids_int64 != 0, T, L.K, c.V, a.inv_temp, r, h.st);
   if (e == cudaSuccess)
-    e = launch_head_prep(h.labels, c.ids_int64 != 0, h.dloss, h.lse_in, h.X, T, c.d, c.V, r, backward ? h.dX : nullptr, f.sms,
-                         h.st);
+    e = launch_head_prep(h.labels, c.ids_int64 != 0, h.dloss, h.lse_in, h.X, T, c.d, c.V, r,
+                         backward ? h.dX : nullptr, f.sms, h.st);
   if (e != cudaSuccess) return cuda_bad(w, "row kernels", e);
 
   auto go = [&](int kind, bool pair, const HeadArgs& args, int64_t m, int64_t ncols, int splits) {

@@ -42,8 +42,7 @@ struct HeadArgs {
   int32_t* status;
   uint64_t timeout_ns;
   int64_t Tp;                // padded rows of the compact buffers
-  int64_t V;                 // vocabulary
-  int64_t v0, vlen;          // this piece of it (kHeadLse: 0, V)
+  int64_t v0, vlen;          // this piece of the vocabulary (kHeadLse: all of it)
   int T, d, K;
   int nsplit;                // kHeadDX: the vocabulary piece is split over this many tiles
   int add;                   // kHeadDX: add into the fp32 sums (0: first piece, overwrite)
@@ -83,8 +82,8 @@ cudaError_t launch_head_entries(const void* teacher, bool teacher_bf16, const vo
 // The list of rows that count and, when some do not, their compact copy of X.
 // labels != NULL: cross entropy; otherwise r.cnt says which rows count.
 // dX != NULL: rows of tokens that do not count are zeroed.
-cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const float* lse, const void* X, int T, int d, int64_t V,
-                             const HeadRows& r, void* dX, int num_sms, cudaStream_t st);
+cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const float* lse, const void* X,
+                             int T, int d, int64_t V, const HeadRows& r, void* dX, int num_sms, cudaStream_t st);
 cudaError_t launch_head_loss(int T, int K, int np, int64_t Tp, float temperature, bool distill, const HeadRows& r,
                              float* loss, float* lse, cudaStream_t st);
 // dX rows of the tokens that count, from the splits' sums.

@@ -13,8 +13,8 @@ cudaError_t prepare_one() {
 
 template <int KIND, int CG, bool TEACHER, int AR = kHBM>
 cudaError_t launch_one(const HeadArgs& a, int grid, cudaStream_t st) {
-  return launch_pdl(head_gemm_kernel<KIND, CG, TEACHER, AR>, dim3(grid), dim3(kHeadThreads), HeadTraits<KIND, CG, AR>::smem_bytes, st,
-                    CG, a);
+  return launch_pdl(head_gemm_kernel<KIND, CG, TEACHER, AR>, dim3(grid), dim3(kHeadThreads),
+                    HeadTraits<KIND, CG, AR>::smem_bytes, st, CG, a);
 }
 
 template <int KIND, int CG, int AR>

@@ -153,8 +153,9 @@ __device__ __forceinline__ bool row_counts(const void* labels, bool ids64, const
 // (Backward) a factor common to all upstream gradients, as in a mean, is
 // taken out of D before D is rounded to bf16.
 __global__ void __launch_bounds__(256) head_prep_kernel(const void* labels, int ids64, const float* dloss,
-                                                        const float* lse, int T, int64_t V, const uint4* __restrict__ X, int vecs,
-                                                        HeadRows r, uint4* __restrict__ dX) {
+                                                        const float* lse, int T, int64_t V,
+                                                        const uint4* __restrict__ X, int vecs, HeadRows r,
+                                                        uint4* __restrict__ dX) {
   __shared__ int s_cnt[8][2];
   __shared__ float s_lo[8], s_hi[8];
   __shared__ int s_on[256], s_off[256];                // tokens of the range that count, and that do not
@@ -373,8 +374,8 @@ cudaError_t launch_head_entries(const void* teacher, bool teacher_bf16, const vo
                     (int)ids64, K, kp, V, inv_temp, r);
 }
 
-cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const float* lse, const void* X, int T, int d, int64_t V,
-                             const HeadRows& r, void* dX, int num_sms, cudaStream_t st) {
+cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const float* lse, const void* X,
+                             int T, int d, int64_t V, const HeadRows& r, void* dX, int num_sms, cudaStream_t st) {
   // few tokens per block, so that a block's copy is short, up to one wave of blocks
   const int blocks = (T + 3) / 4 < 8 * num_sms ? (T + 3) / 4 : 8 * num_sms;
   return launch_pdl(head_prep_kernel, dim3(blocks), dim3(256), 0, st, 1, labels, (int)ids64, dloss, lse, T, V,
@@ -384,8 +385,8 @@ cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss,
 cudaError_t launch_head_loss(int T, int K, int np, int64_t Tp, float temperature, bool distill, const HeadRows& r,
                              float* loss, float* lse, cudaStream_t st) {
   // few blocks: more threads each
-  return launch_pdl(head_loss_kernel, dim3((T + 3) / 4), dim3(T <= 1024 ? 1024 : 256), 0, st, 1, T, K, np, Tp, temperature, (int)distill,
-                    r, loss, lse);
+  return launch_pdl(head_loss_kernel, dim3((T + 3) / 4), dim3(T <= 1024 ? 1024 : 256), 0, st, 1, T, K, np, Tp, temperature,
+                    (int)distill, r, loss, lse);
 }
 
 cudaError_t launch_head_dx(int T, int d, int nsplit, int64_t Tp, float out_scale, const HeadRows& r, void* dX,
