@@ -376,8 +376,10 @@ cudaError_t launch_head_entries(const void* teacher, bool teacher_bf16, const vo
 
 cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const float* lse, const void* X,
                              int T, int d, int64_t V, const HeadRows& r, void* dX, int num_sms, cudaStream_t st) {
-  // few tokens per block, so that a block's copy is short, up to one wave of blocks
-  const int blocks = (T + 3) / 4 < 8 * num_sms ? (T + 3) / 4 : 8 * num_sms;
+  // few tokens per block, so that a block's copy is short, up to one wave of
+  // blocks; fewer when T is large, since every block reads all T tokens' labels
+  const int most = (T <= 32768 ? 8 : 2) * num_sms;
+  const int blocks = (T + 3) / 4 < most ? (T + 3) / 4 : most;
   return launch_pdl(head_prep_kernel, dim3(blocks), dim3(256), 0, st, 1, labels, (int)ids64, dloss, lse, T, V,
                     reinterpret_cast<const uint4*>(X), d / 8, r, reinterpret_cast<uint4*>(dX));
 }

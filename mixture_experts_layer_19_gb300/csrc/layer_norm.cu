@@ -913,6 +913,13 @@ int64_t bwd_blocks(int64_t rows, int threads, int sms) {
 }
 int64_t long_slices(int64_t rows) { return std::min<int64_t>(rows, 32); }
 
+// A launch's dynamic shared memory past the 48 KB that need no leave.
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes) {
+  if (bytes <= 48 << 10) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <class XT, class WT, int VW, int VPT>
 cudaError_t fwd_go(const void* x, const void* w, const void* b, int64_t rows, int d, float eps, void* y, float* mean,
                    float* rstd, const Shape& s, int sms, cudaStream_t st) {
@@ -940,7 +947,7 @@ cudaError_t fwd_rows_go(const void* x, const void* w, const void* b, bool w_f32,
                         float eps, void* y, float* mean, float* rstd, int sms, cudaStream_t st) {
   const int smem = d * 8;
   auto kernel = ln_fwd_rows_kernel<XT, NV>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
   constexpr int kRowWarps = row_warps(NV);
   const int64_t groups = kRowWarps / wpr;
@@ -954,7 +961,7 @@ cudaError_t bwd_depth_go(const void* dy, const void* x, const void* w, bool w_f3
                          cudaStream_t st) {
   const int smem = DEPTH * 2 * VPT * s.threads * 16;
   auto kernel = ln_bwd_rows_kernel<XT, VPT, DEPTH>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3(s.threads), smem, st, 1, (const uint4*)dy, (const uint4*)x, w,
                     w_f32, mean, rstd, rows, d, (uint4*)dx, pw, pb);
@@ -977,7 +984,7 @@ cudaError_t bwd_odd_depth_go(const void* dy, const void* x, const void* w, bool 
                              int64_t blocks, cudaStream_t st) {
   const int smem = DEPTH * 2 * (d * (int)sizeof(XT) / 16 + 2) * 16;
   auto kernel = ln_bwd_odd_kernel<XT, EPT, DEPTH>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3(s.threads), smem, st, 1, (const XT*)dy, (const XT*)x, w, w_f32,
                     mean, rstd, rows, d, (XT*)dx, pw, pb);
@@ -1009,7 +1016,7 @@ cudaError_t fwd_odd_go(const void* x, const void* w, const void* b, bool w_f32, 
                        void* y, float* mean, float* rstd, int sms, cudaStream_t st) {
   auto kernel = ln_fwd_odd_kernel<XT>;
   const int64_t groups = kOddWarps / wpr;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, d * 8);
+  cudaError_t e = allow_smem(kernel, d * 8);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>((rows + groups - 1) / groups, sms)), dim3(kOddWarps * 32),
                     d * 8, st, 1, (const XT*)x, w, b, w_f32, rows, d, wpr, eps, (XT*)y, mean, rstd);

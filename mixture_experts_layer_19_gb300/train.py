@@ -23,6 +23,7 @@ import functools
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import moe
 from .moe import MOE_DEBUG_STALL_TEST, moe_head_config_t  # noqa: F401  (MOE_DEBUG_STALL_TEST: tests)
@@ -74,14 +75,22 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
 _status = {}
 
 
-def _status_word(index: int) -> torch.Tensor:
-    """One device word per GPU that receives a kernel's timeout code."""
+def _status_word(index: int) -> Optional[torch.Tensor]:
+    """One device word per GPU that receives a kernel's timeout code.  (It cannot be made while the
+    stream is being captured: a graph captured before any other call reports no timeouts.)"""
     s = _status.get(index)
     if s is None:
+        if torch.cuda.is_current_stream_capturing():
+            return None
         s = torch.zeros((1,), dtype=_I32, device=torch.device("cuda", index))
         torch.cuda.current_stream(index).synchronize()   # zeroed before any stream's kernels use it
         _status[index] = s
     return s
+
+
+def _status_ptr(index: int) -> Optional[int]:
+    s = _status_word(index)
+    return None if s is None else s.data_ptr()
 
 
 def device_status(device=0) -> int:
@@ -184,6 +193,7 @@ class _LayerNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -278,7 +288,7 @@ def _head_forward(call, name, cfg, X, args, index):
     n = _head_workspace_bytes(cfg.T, cfg.V, cfg.d, cfg.K, 0, False, index)
     ws = _workspace(n, X.device)
     _check(call(ctypes.byref(cfg), *args, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n,
-                _status_word(index).data_ptr(), _raw_stream(index)), name)
+                _status_ptr(index), _raw_stream(index)), name)
     return loss, lse
 
 
@@ -310,7 +320,7 @@ def _head_backward(call, name, cfg, X, W, args, need_dX, need_dW, index):
     n = _head_workspace_bytes(cfg.T, cfg.V, cfg.d, cfg.K, cfg.piece, True, index)
     ws = _workspace(n, X.device)
     _check(call(ctypes.byref(cfg), *args, dX.data_ptr() if need_dX else None, dW.data_ptr() if need_dW else None,
-                ws.data_ptr(), n, _status_word(index).data_ptr(), _raw_stream(index)), name)
+                ws.data_ptr(), n, _status_ptr(index), _raw_stream(index)), name)
     return dX, dW
 
 
@@ -367,6 +377,7 @@ class _CrossEntropyFunction(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         X, W, labels, lse = ctx.saved_tensors
         dX, dW = cross_entropy_backward(dloss.contiguous(), X, W, labels, lse, need_dX=ctx.needs_input_grad[0],
@@ -384,6 +395,7 @@ class _DistillFunction(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         X, W, teacher, ids, lse = ctx.saved_tensors
         dX, dW = distill_backward(dloss.contiguous(), X, W, teacher, ids, lse, ctx.temperature,

@@ -244,6 +244,14 @@ def test_cross_entropy(train, T, d, V, dtype):
     check_head(train, X, W, torch.full((T,), 1.0 / max(1, int(on.sum()))), (P, on, np.zeros(T)), labels=labels)
 
 
+def test_cross_entropy_many_tokens(train):
+    T, d, V = 40000, 64, 300
+    X, W, g = head_inputs(T, d, V, seed=2)
+    labels = labels_for(T, V, g, ignored=0.5)
+    P, on = train_ref.one_hot_targets(labels.numpy(), V)
+    check_head(train, X, W, torch.full((T,), 1.0 / int(on.sum())), (P, on, np.zeros(T)), labels=labels)
+
+
 @pytest.mark.parametrize("piece", [256, 300, 512, 4096])
 @pytest.mark.parametrize("T", [40, 300])
 def test_cross_entropy_in_pieces_with_weights(train, T, piece):
