@@ -100,7 +100,7 @@ struct Layout {
   int64_t Tp, piece, ldl;   // padded rows, columns of one piece, leading dimension of the D piece
   int K, nsplit;
   bool pair_z, pair_x, pair_w;   // CTA pairs for the logits, dX and dW products
-  int arows;                // rows of A per CTA in the logits products
+  int arows, bn;            // rows of A per CTA and columns of a tile in the logits products
   bool sums;                // dX needs the fp32 sums (several pieces or splits)
   int64_t blocks;           // blocks of 128 vocabulary columns
   size_t counts, scale, rec, inv, ids, probs, first, cnt, plogp, xc, part, zt, dl, acc, total;
@@ -135,14 +135,16 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
     L.ldl = L.piece;
     const int64_t cols = std::min<int64_t>(L.piece, c.V);
     // dX has few tiles when T is small: its K, the piece, is split until they
-    // fill the SMs.  Splitting costs another launch (12 slices) and each split
-    // the traffic of its fp32 sums (about 2)
+    // fill the SMs.  Splitting costs another launch (12 slices), and each split
+    // the traffic of its fp32 sums, written and read at 5 TB/s, and a load in
+    // that launch's chain.
+    const double per_split = 0.25 + 6e-6 * (double)c.T * c.d;
     const int64_t nkb = ceil_div(cols, 64);
     double best = 0;
-    for (int pair = 0; pair < 2; ++pair)
-      for (int s = 1; s <= 16 && s <= nkb; ++s) {
+    for (int pair = 0; pair < (c.T > 128 ? 2 : 1); ++pair)
+      for (int s = 1; s <= 48 && s <= nkb; ++s) {
         const double cost = tiles_cost(c.T, c.d, (double)nkb / s, kEpiGrad, s, pair != 0, sms, pairs) +
-                            (s > 1 ? 12.0 + 2.0 * (s - 1) : 0.0);
+                            (s > 1 ? 12.0 + per_split * (s - 1) : 0.0);
         if ((s == 1 && !pair) || cost < best) {
           best = cost;
           L.nsplit = s;
@@ -157,7 +159,15 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
   }
   L.pair_z = better_as_pair(c.T, backward ? std::min<int64_t>(L.piece, c.V) : c.V, (double)ceil_div(c.d, 64),
                             kEpiLogits, sms, pairs);
+  // One row tile waits for W: no pair (its second half would have no rows).  Up
+  // to 64 tokens fetch no more rows of X than they have, and where the vocabulary
+  // has fewer tiles of 256 columns than there are SMs, narrower ones let more
+  // SMs fetch (64 x 4096 x 8192 backward: 67.7 us against 60.2; 224 columns for 32768
+  // entries, 147 tiles instead of 128, gained nothing).
+  if (c.T <= 128) L.pair_z = false;
   L.arows = L.pair_z || c.T > 64 ? 128 : c.T > 16 ? 64 : 16;
+  const int64_t zcols = backward ? std::min<int64_t>(L.piece, c.V) : c.V;
+  L.bn = L.arows < 128 ? (int)std::min<int64_t>(kHeadBN, up(ceil_div(zcols, sms), 64)) : kHeadBN;
   size_t o = 0;
   auto take = [&o](size_t bytes) {
     const size_t at = o;
@@ -176,7 +186,7 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
   L.plogp = distill ? take(c.T * 4) : 0;
   L.xc = take((size_t)L.Tp * c.d * 2);
   if (!backward) {
-    L.part = take((size_t)((c.V + kHeadBN - 1) / kHeadBN) * 2 * L.Tp * 8);
+    L.part = take((size_t)ceil_div(c.V, L.bn) * 2 * L.Tp * 8);
     L.zt = take((size_t)c.T * L.K * 4);
   } else {
     L.dl = take((size_t)L.Tp * L.ldl * 2);
@@ -288,12 +298,13 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   a.d = c.d;
   a.K = L.K;
   a.nsplit = 1;
+  a.bn = L.bn;
   a.inv_temp = 1.0f / temp;
   a.out_scale = temp;
   a.stall = (c.debug_flags & MOE_DEBUG_STALL_TEST) ? 1 : 0;
 
   bool ok = map_k(&a.mapA0, h.X, c.d, T, c.d, L.arows) && map_k(&a.mapA1, r.Xc, c.d, L.Tp, c.d, L.arows) &&
-            map_k(&a.mapB0, h.W, c.d, c.V, c.d, L.pair_z ? 128 : 256);
+            map_k(&a.mapB0, h.W, c.d, c.V, c.d, L.pair_z ? 128 : L.bn);
   HeadArgs ax{}, aw{};
   if (backward) {
     a.dl = static_cast<__nv_bfloat16*>(r.dl);
@@ -320,7 +331,7 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   if (e != cudaSuccess) return cuda_bad(w, "row kernels", e);
 
   auto go = [&](int kind, bool pair, const HeadArgs& args, int64_t m, int64_t ncols, int splits) {
-    const int64_t tiles = ceil_div(m, pair ? 256 : 128) * ceil_div(ncols, kHeadBN) * splits;
+    const int64_t tiles = ceil_div(m, pair ? 256 : 128) * ceil_div(ncols, kind <= kHeadDl ? L.bn : kHeadBN) * splits;
     const int64_t workers = std::min<int64_t>(tiles, pair ? f.pairs : f.sms);
     return head_gemm_launch(kind, pair, L.arows, args, (int)workers * (pair ? 2 : 1), h.st);
   };
@@ -329,7 +340,7 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
     a.vlen = c.V;
     e = go(kHeadLse, L.pair_z, a, T, c.V, 1);
     if (e == cudaSuccess)
-      e = launch_head_loss(T, L.K, (int)(2 * ceil_div(c.V, kHeadBN)), L.Tp, temp, distill, r, h.loss, h.lse_out, h.st);
+      e = launch_head_loss(T, L.K, (int)(2 * ceil_div(c.V, L.bn)), L.Tp, temp, distill, r, h.loss, h.lse_out, h.st);
     return e == cudaSuccess ? MOE_OK : cuda_bad(w, "launch", e);
   }
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += L.piece) {

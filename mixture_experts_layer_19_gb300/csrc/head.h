@@ -44,6 +44,7 @@ struct HeadArgs {
   int64_t Tp;                // padded rows of the compact buffers
   int64_t v0, vlen;          // this piece of the vocabulary (kHeadLse: all of it)
   int T, d, K;
+  int bn;                    // kHeadLse, kHeadDl: columns of a tile, 64, 128, 192 or 256 (arows < 128)
   int nsplit;                // kHeadDX: the vocabulary piece is split over this many tiles
   int add;                   // kHeadDX: add into the fp32 sums (0: first piece, overwrite)
   float inv_temp;            // 1 / temperature

@@ -70,17 +70,25 @@ struct HeadTile {
   int split;
 };
 
-template <int KIND, int CG>
+// Columns of a tile: 256; up to 64 tokens' logits products take what the call
+// says (64, 128, 192 or 256).
+template <int AR>
+__device__ __forceinline__ int head_bn(const HeadArgs& g) {
+  return AR == kHBM ? kHeadBN : g.bn;
+}
+
+template <int KIND, int CG, int AR>
 __device__ __forceinline__ int64_t head_tiles(const HeadArgs& g, int na, int& MT, int& NT) {
   constexpr int TM = kHBM * CG;
   const int64_t mrows = KIND == kHeadDW ? g.vlen : na;
-  const int64_t ncols = (KIND == kHeadLse || KIND == kHeadDl) ? g.vlen : g.d;
+  const int64_t ncols = KIND <= kHeadDl ? g.vlen : g.d;
+  const int bn = head_bn<AR>(g);
   MT = (int)((mrows + TM - 1) / TM);
-  NT = (int)((ncols + kHeadBN - 1) / kHeadBN);
+  NT = (int)((ncols + bn - 1) / bn);
   return (int64_t)MT * NT * (KIND == kHeadDX ? g.nsplit : 1);
 }
 
-template <int KIND, int CG>
+template <int KIND, int CG, int AR>
 __device__ __forceinline__ HeadTile head_tile(const HeadArgs& g, int na, int MT, int NT, int64_t w) {
   HeadTile t;
   t.split = 0;
@@ -98,7 +106,7 @@ __device__ __forceinline__ HeadTile head_tile(const HeadArgs& g, int na, int MT,
     mt = local - nt * MT;
   }
   t.row0 = mt * (kHBM * CG);
-  t.col0 = nt * kHeadBN;
+  t.col0 = nt * head_bn<AR>(g);
   t.kb0 = 0;
   if (KIND == kHeadDX) {
     const int nkb = (int)((g.vlen + kHBK - 1) / kHBK);
@@ -226,7 +234,8 @@ struct HeadRow {
     gr = __int_as_float(q.w);
   }
   __device__ __forceinline__ void find_first(const HeadArgs& g, int64_t vcol) {
-    if constexpr (TEACHER) e = tok >= 0 ? (int)__ldg(g.first + (int64_t)tok * g.blocks + vcol / 128) : 0;
+    if constexpr (TEACHER)
+      e = tok >= 0 ? (int)__ldg(g.first + (int64_t)tok * g.blocks + min(vcol / 128, g.blocks - 1)) : 0;
   }
   __device__ __forceinline__ void load(const HeadArgs& g, int i, int& id, float& p) {
     const bool in = tok >= 0 && i < cnt;
@@ -237,6 +246,7 @@ struct HeadRow {
     if constexpr (TEACHER) {
       load(g, e, id0, p0);
       load(g, e + 1, id1, p1);
+      while (id0 < vcol) next(g);        // the table's block may start before the column
     } else {
       e = 0;
       id0 = tok >= 0 && cnt >= vcol ? cnt : INT_MAX;
@@ -329,7 +339,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
 
   const int na = *g.n_active;
   int MT, NT;
-  const int64_t nwork = head_tiles<KIND, CG>(g, na, MT, NT);
+  const int64_t nwork = head_tiles<KIND, CG, AR>(g, na, MT, NT);
+  const int bn = head_bn<AR>(g);
   const int64_t w0 = blockIdx.x / CG;
   const int64_t wstep = gridDim.x / CG;
 
@@ -345,12 +356,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
       uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
       bool ok = true;
       for (int64_t w = w0; w < nwork && ok && !g.stall; w += wstep) {
-        const HeadTile t = head_tile<KIND, CG>(g, na, MT, NT, w);
+        const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
         const int64_t arow = t.row0 + rank * kHBM;          // this CTA's rows of A
         const int64_t bcol = t.col0 + rank * TR::b_rows;    // and columns of B
         for (int kb = 0; kb < t.nkb; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1, wc)) { ok = false; break; }
-          if (leader) mbar_arrive_expect_tx(&full[s], TR::stage_bytes * CG);
+          if (leader) mbar_arrive_expect_tx(&full[s], TR::a_bytes * CG + bn * kHBK * 2);
           uint8_t* sa = stage_base + s * TR::stage_bytes;
           uint8_t* sb = sa + TR::a_bytes;
           const int32_t k0 = (t.kb0 + kb) * kHBK;
@@ -395,11 +406,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc = idesc_bf16(kHBM * CG, kHeadBN, TR::a_mn ? 1 : 0, TR::b_mn ? 1 : 0);
+      const uint32_t idesc = idesc_bf16(kHBM * CG, bn, TR::a_mn ? 1 : 0, TR::b_mn ? 1 : 0);
       uint32_t s = 0, ph = 0, acc = 0, aph = 0;
       bool ok = true;
       for (int64_t w = w0; w < nwork && ok; w += wstep) {
-        const HeadTile t = head_tile<KIND, CG>(g, na, MT, NT, w);
+        const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
         if (t.nkb == 0) continue;
         const int phases = head_phases<KIND>(t.nkb);
         for (int p = 0; p < phases && ok; ++p) {
@@ -455,20 +466,21 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     const int sub = lane >> 3, chunk = lane & 7;                  // coalesced writes: row within 4, 16-byte chunk
     [[maybe_unused]] const float sc = KIND >= kHeadDX ? *g.scale * g.out_scale : 1.0f;
     [[maybe_unused]] HeadRow<TEACHER> cur, nxt;
+    const int half = bn / 2;                                      // columns of a warp: 32, 64, 96 or 128
     if constexpr (KIND <= kHeadDl) {
       if (w0 < nwork) {
-        const HeadTile t = head_tile<KIND, CG>(g, na, MT, NT, w0);
-        const int64_t vcol = g.v0 + t.col0 + h * 128;
+        const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w0);
+        const int64_t vcol = g.v0 + t.col0 + h * half;
         nxt.fetch_record(g, t.row0 + rank * kHBM + 32 * q + lane, na);
         nxt.find_first(g, vcol);
         nxt.fetch_entries(g, vcol);
       }
     }
     for (int64_t w = w0; w < nwork; w += wstep) {
-      const HeadTile t = head_tile<KIND, CG>(g, na, MT, NT, w);
+      const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
       const int64_t rowq = t.row0 + rank * kHBM + 32 * q;         // the warp's first row
       const int64_t row = rowq + lane;                            // this lane's row
-      const int64_t colh = t.col0 + h * 128;                      // the warp's first column
+      const int64_t colh = t.col0 + h * half;                     // the warp's first column
 
       if constexpr (KIND <= kHeadDl) {
         cur = nxt;
@@ -476,22 +488,23 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         const bool more = w + wstep < nwork;
         int64_t nvcol = 0;
         if (more) {
-          const HeadTile n = head_tile<KIND, CG>(g, na, MT, NT, w + wstep);
-          nvcol = g.v0 + n.col0 + h * 128;
+          const HeadTile n = head_tile<KIND, CG, AR>(g, na, MT, NT, w + wstep);
+          nvcol = g.v0 + n.col0 + h * half;
           nxt.fetch_record(g, n.row0 + rank * kHBM + 32 * q + lane, na);
         }
-        const int64_t left = g.vlen - colh;                       // columns inside the vocabulary
-        const int last = (int)vcol + 128;                         // ids below it are this block's
+        const int64_t left = min((int64_t)half, g.vlen - colh);   // its columns inside the vocabulary
+        const int last = (int)vcol + half;                        // ids below it are this block's
         if constexpr (KIND == kHeadLse) {
-          float z[128];
+          float z[128] = {};
           const int phases = head_phases<KIND>(t.nkb);
           bool ok = true;
           for (int p = 0; p < phases; ++p) {
             if (!mbar_wait(&tfull[acc], aph, wc)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * 128;
+            const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * half;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
+              if (c * 32 >= half) break;
               uint32_t r[32];
               tmem_ld32(tb + c * 32, r);
               tmem_ld_wait();
@@ -535,25 +548,27 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int i = 0; i < 128; ++i) s4[i & 3] += ex2_approx(fmaf(z[i], c2, -mb));
-          g.part[(2 * (t.col0 / kHeadBN) + h) * g.Tp + row] =
+          g.part[(2 * (t.col0 / bn) + h) * g.Tp + row] =
               make_float2(m * g.inv_temp, (s4[0] + s4[1]) + (s4[2] + s4[3]));
         } else {
           if (!mbar_wait(&tfull[acc], aph, wc)) break;
           tc_fence_after();
-          const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * 128;
+          const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * half;
           uint32_t r[32];
           tmem_ld32(tb, r);
           __nv_bfloat16* out = g.dl + (rowq + sub) * g.ldl + colh + chunk * 8;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {                           // 32 columns at a time, stored by 64
+            if (c * 32 >= half) break;
             tmem_ld_wait();
             float v[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = ex2_approx(fmaf(__uint_as_float(r[i]), c2, -cur.rl));
-            if (c < 3) tmem_ld32(tb + (c + 1) * 32, r);
+            if (c * 32 + 32 < half) tmem_ld32(tb + (c + 1) * 32, r);
             else release(acc);
-            while (__any_sync(0xffffffffu, cur.id0 < last - 96 + c * 32)) {
-              const bool hit = cur.id0 < last - 96 + c * 32;
+            const int until = (int)vcol + c * 32 + 32;
+            while (__any_sync(0xffffffffu, cur.id0 < until)) {
+              const bool hit = cur.id0 < until;
               const int col = hit ? cur.id0 - (int)vcol - c * 32 : -1;
               const float p = cur.p0;
 #pragma unroll
@@ -561,22 +576,25 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
                 if (i == col) v[i] -= p;
               if (hit) cur.next(g);
             }
-            if (c == 1 && more) nxt.find_first(g, nvcol);
+            if (c == 0 && more) nxt.find_first(g, nvcol);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= cur.gr;
-            if (left < 128 || rowq + 32 > na) {                   // zeros past the vocabulary and the rows that count
+            if (left < half || rowq + 32 > na) {                   // zeros past the vocabulary and the rows that count
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (c * 32 + i >= left || cur.tok < 0) v[i] = 0.0f;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) stage_put(stg, lane, (c & 1) * 4 + k, pack8(v + 8 * k));
-            if (c & 1) {
+            if ((c & 1) || c * 32 + 32 >= half) {
               __syncwarp();
+              const int x = (c & ~1) * 32 + chunk * 8;
+              if (x < half && colh + x < g.ldl) {
 #pragma unroll
-              for (int it = 0; it < 8; ++it)
-                *reinterpret_cast<uint4*>(out + (int64_t)(4 * it) * g.ldl + (c - 1) * 32) =
-                    stage_get(stg, 4 * it + sub, chunk);
+                for (int it = 0; it < 8; ++it)
+                  *reinterpret_cast<uint4*>(out + (int64_t)(4 * it) * g.ldl + (c & ~1) * 32) =
+                      stage_get(stg, 4 * it + sub, chunk);
+              }
               __syncwarp();
             }
           }

@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(256) head_dx_kernel(int d, int nsplit, int64_t
     const int64_t row = i / vecs;
     const int c = (int)(i - row * vecs);
     float4 a = acc[i];
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 1; s < nsplit; ++s) {
       const float4 b = acc[(s * Tp + row) * vecs + c];
       a.x += b.x;
