@@ -113,18 +113,26 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // its epilogue (epi slices, overlapped with the next tile's products), and the last
 // epilogue, which nothing overlaps.  A single CTA's slice moves 48 KB into its SM
 // where a pair moves 32 per SM, and takes 1.1 times as long (4096 x 7168 x
-// 65536 forward: 2508 us against 2393).
-constexpr double kEpiLogits = 12, kEpiGrad = 6, kStart = 16;
-double tiles_cost(int64_t m, int64_t ncols, double nkb, double epi, int splits, bool pair, int sms, int pairs) {
-  const int64_t tiles = ceil_div(m, pair ? 256 : 128) * ceil_div(ncols, kHeadBN) * splits;
-  return (double)ceil_div(tiles, pair ? pairs : sms) * std::max((pair ? 1.0 : 1.1) * nkb, epi) + kStart;
-}
-bool better_as_pair(int64_t m, int64_t ncols, double nkb, double epi, int sms, int pairs) {
-  return tiles_cost(m, ncols, nkb, epi, 1, true, sms, pairs) <= tiles_cost(m, ncols, nkb, epi, 1, false, sms, pairs);
-}
+// 65536 forward: 2508 us against 2393), 1.3 where rows do not end on 32 bytes
+// (520 x 1000 x 50001 backward: 197 against 175).  A pair's epilogues wait for
+// each other (1000 x 256 x 30000 forward: 34.5 us against 28.2 with single CTAs).
+constexpr double kEpiLogits = 12, kEpiGrad = 6, kEpiPair = 1.25, kStart = 16;
+struct Cost {
+  int sms, pairs;
+  double single;     // a single CTA's slice
+  double of(int64_t m, int64_t ncols, double nkb, double epi, int splits, bool pair) const {
+    const int64_t tiles = ceil_div(m, pair ? 256 : 128) * ceil_div(ncols, kHeadBN) * splits;
+    const double tile = pair ? std::max(nkb, kEpiPair * epi) : std::max(single * nkb, epi);
+    return (double)ceil_div(tiles, pair ? pairs : sms) * tile + kStart;
+  }
+  bool pair_pays(int64_t m, int64_t ncols, double nkb, double epi) const {
+    return of(m, ncols, nkb, epi, 1, true) <= of(m, ncols, nkb, epi, 1, false);
+  }
+};
 
 Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, int pairs) {
   Layout L{};
+  const Cost cost{sms, pairs, c.d % 16 == 0 ? 1.1 : 1.3};
   L.K = distill ? c.K : 1;
   L.Tp = std::max<int64_t>(up(c.T, kHeadRowPad), kHeadRowPad);
   L.nsplit = 1;
@@ -143,22 +151,22 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
     double best = 0;
     for (int pair = 0; pair < (c.T > 128 ? 2 : 1); ++pair)
       for (int s = 1; s <= 48 && s <= nkb; ++s) {
-        const double cost = tiles_cost(c.T, c.d, (double)nkb / s, kEpiGrad, s, pair != 0, sms, pairs) +
-                            (s > 1 ? 12.0 + per_split * (s - 1) : 0.0);
-        if ((s == 1 && !pair) || cost < best) {
-          best = cost;
+        const double t = cost.of(c.T, c.d, (double)nkb / s, kEpiGrad, s, pair != 0) +
+                         (s > 1 ? 12.0 + per_split * (s - 1) : 0.0);
+        if ((s == 1 && !pair) || t < best) {
+          best = t;
           L.nsplit = s;
           L.pair_x = pair != 0;
         }
       }
     // dW of few tokens is bound by its writes, which single CTAs, each on its own
-    // tile, keep going better than pairs (64 x 7168 x 131072: 383 us against 503);
-    // from 256 tokens on the products count (875 against 887)
-    L.pair_w = c.T >= 256 && better_as_pair(cols, c.d, (double)ceil_div(c.T, 64), kEpiGrad, sms, pairs);
+    // tile, keep going better than pairs (64 x 7168 x 131072: 383 us against 503,
+    // 300 x 2048 x 32768 98 against 105; 520 x 1000 x 50001 143 against 123)
+    L.pair_w = c.T >= 384 && cost.pair_pays(cols, c.d, (double)ceil_div(c.T, 64), kEpiGrad);
     L.sums = L.nsplit > 1 || L.piece < c.V;
   }
-  L.pair_z = better_as_pair(c.T, backward ? std::min<int64_t>(L.piece, c.V) : c.V, (double)ceil_div(c.d, 64),
-                            kEpiLogits, sms, pairs);
+  const int64_t zcols = backward ? std::min<int64_t>(L.piece, c.V) : c.V;
+  L.pair_z = cost.pair_pays(c.T, zcols, (double)ceil_div(c.d, 64), kEpiLogits);
   // One row tile waits for W: no pair (its second half would have no rows).  Up
   // to 64 tokens fetch no more rows of X than they have, and where the vocabulary
   // has fewer tiles of 256 columns than there are SMs, narrower ones let more
@@ -166,7 +174,6 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
   // entries, 147 tiles instead of 128, gained nothing).
   if (c.T <= 128) L.pair_z = false;
   L.arows = L.pair_z || c.T > 64 ? 128 : c.T > 16 ? 64 : 16;
-  const int64_t zcols = backward ? std::min<int64_t>(L.piece, c.V) : c.V;
   L.bn = L.arows < 128 ? (int)std::min<int64_t>(kHeadBN, up(ceil_div(zcols, sms), 64)) : kHeadBN;
   size_t o = 0;
   auto take = [&o](size_t bytes) {
