@@ -28,8 +28,8 @@
 // The tensor cores add into fp32 accumulators with truncation, which pulls a
 // 7168-long dot product towards zero by about 7e-6 of its value (measured
 // against 64 bits).  The loss is a difference of logits, so kHeadLse ends an
-// accumulator every kLseChunk of K and adds the parts in registers, rounded
-// to nearest.  The gradients are rounded to bf16 and do not need it.
+// accumulator every kLseChunk slices of K and adds the parts in registers,
+// rounded to nearest.  The gradients are rounded to bf16 and do not need it.
 #pragma once
 #include "head.h"
 #include "pdl.cuh"
@@ -41,7 +41,8 @@ constexpr int kHBM = 128;                    // rows per CTA
 constexpr int kHBK = 64;                     // K slice (128 bytes of bf16)
 constexpr int kHeadThreads = 320;
 constexpr int kHeadEpiWarps = 8;
-constexpr int kLseChunk = 16;                // K slices per accumulator of kHeadLse (1024)
+constexpr int kLseChunk = 16;                // K slices per accumulator of kHeadLse (1024), and
+constexpr int kLseChunkFew = 8;              // of up to 64 tokens (512), whose epilogues have the time
 
 // AR rows of A are fetched per CTA: 128, or 16 or 64 when the call has no more
 // tokens.  The product still covers 128 rows -- those past AR read whatever
@@ -119,10 +120,11 @@ __device__ __forceinline__ HeadTile head_tile(const HeadArgs& g, int na, int MT,
   return t;
 }
 
-// Accumulators (TMEM phases) of one tile, and the K slices of phase i.
-template <int KIND>
+// Accumulators (TMEM phases) of one tile.
+template <int KIND, int AR>
 __device__ __forceinline__ int head_phases(int nkb) {
-  return KIND == kHeadLse ? (nkb + kLseChunk - 1) / kLseChunk : 1;
+  constexpr int chunk = AR == kHBM ? kLseChunk : kLseChunkFew;
+  return KIND == kHeadLse ? (nkb + chunk - 1) / chunk : 1;
 }
 
 // ---------------------------------------------------------------- pair (cta_group::2) pieces
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
       for (int64_t w = w0; w < nwork && ok; w += wstep) {
         const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
         if (t.nkb == 0) continue;
-        const int phases = head_phases<KIND>(t.nkb);
+        const int phases = head_phases<KIND, AR>(t.nkb);
         for (int p = 0; p < phases && ok; ++p) {
           const int k_lo = (int)((int64_t)t.nkb * p / phases), k_hi = (int)((int64_t)t.nkb * (p + 1) / phases);
           if (!mbar_wait(&tempty[acc], aph ^ 1, wc)) { ok = false; break; }
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         const int last = (int)vcol + half;                        // ids below it are this block's
         if constexpr (KIND == kHeadLse) {
           float z[128] = {};
-          const int phases = head_phases<KIND>(t.nkb);
+          const int phases = head_phases<KIND, AR>(t.nkb);
           bool ok = true;
           for (int p = 0; p < phases; ++p) {
             if (!mbar_wait(&tfull[acc], aph, wc)) { ok = false; break; }
