@@ -2,7 +2,7 @@
 // workspace layout, tensor maps and the kernel sequence of cross entropy and
 // distillation, forward and backward.
 //
-// Forward   [teacher entries] -> row list, compact X -> logits + softmax
+// Forward   [teacher entries] -> [row list, compact X] -> logits + softmax
 //           statistics GEMM -> losses
 // Backward  [teacher entries] -> row list, compact X -> per vocabulary piece:
 //           D GEMM, dX GEMM (fp32 sums), dW GEMM -> dX rounding
@@ -332,7 +332,10 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   cudaError_t e = cudaSuccess;
   if (distill)
     e = launch_head_entries(h.teacher, c.teacher_bf16 != 0, h.ids, c.ids_int64 != 0, T, L.K, c.V, a.inv_temp, r, h.st);
-  if (e == cudaSuccess)
+  // One row tile forward takes as long with every token's row as without some
+  // of them, and rows do not mix: no list of the rows that count is made.
+  const bool listed = backward || T > 128;
+  if (e == cudaSuccess && listed)
     e = launch_head_prep(h.labels, c.ids_int64 != 0, h.dloss, h.lse_in, h.X, T, c.d, c.V, r,
                          backward ? h.dX : nullptr, f.sms, h.st);
   if (e != cudaSuccess) return cuda_bad(w, "row kernels", e);
@@ -345,9 +348,19 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
   if (!backward) {
     a.v0 = 0;
     a.vlen = c.V;
+    HeadRows rl = r;
+    if (!listed) {
+      a.n_active = nullptr;
+      a.labels = h.labels;
+      a.cnt = r.cnt;
+      a.ids64 = c.ids_int64 != 0;
+      a.V = c.V;
+      rl.inv = nullptr;
+    }
     e = go(kHeadLse, L.pair_z, a, T, c.V, 1);
     if (e == cudaSuccess)
-      e = launch_head_loss(T, L.K, (int)(2 * ceil_div(c.V, L.bn)), L.Tp, temp, distill, r, h.loss, h.lse_out, h.st);
+      e = launch_head_loss(h.labels, c.ids_int64 != 0, T, c.V, L.K, (int)(2 * ceil_div(c.V, L.bn)), L.Tp, temp, distill,
+                           rl, h.loss, h.lse_out, h.st);
     return e == cudaSuccess ? MOE_OK : cuda_bad(w, "launch", e);
   }
   for (int64_t v0 = 0; v0 < c.V && e == cudaSuccess; v0 += L.piece) {

@@ -24,7 +24,12 @@ struct HeadArgs {
   CUtensorMap mapA1;         // kHeadLse / kHeadDl: the compacted copy of X
   CUtensorMap mapB0;         // B operand; kHeadDW: X itself
   CUtensorMap mapB1;         // kHeadDW: the compacted copy of X
-  const int32_t* n_active;   // [1] compact rows
+  const int32_t* n_active;   // [1] compact rows; NULL: every token has its own row (kHeadLse, one row tile),
+                             //   and what counts is read from labels or cnt
+  const void* labels;        // [T] int32, or int64 with ids64
+  const int32_t* cnt;        // [T] distillation: entries in use
+  int ids64;
+  int64_t V;
   const int4* rec;           // [Tp] of each compact row: token, label (or teacher entries in use), and, as float
                              //   bits for kHeadDl, log-sum-exp in base 2 and upstream gradient / *scale
   const int32_t* ids;        // distillation: [T, K] entries in use of each token, ids ascending
@@ -85,8 +90,10 @@ cudaError_t launch_head_entries(const void* teacher, bool teacher_bf16, const vo
 // dX != NULL: rows of tokens that do not count are zeroed.
 cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss, const float* lse, const void* X,
                              int T, int d, int64_t V, const HeadRows& r, void* dX, int num_sms, cudaStream_t st);
-cudaError_t launch_head_loss(int T, int K, int np, int64_t Tp, float temperature, bool distill, const HeadRows& r,
-                             float* loss, float* lse, cudaStream_t st);
+// r.inv == NULL: no list of rows was made; token t has row t, and labels (or r.cnt) say whether it counts.
+cudaError_t launch_head_loss(const void* labels, bool ids64, int T, int64_t V, int K, int np, int64_t Tp,
+                             float temperature, bool distill, const HeadRows& r, float* loss, float* lse,
+                             cudaStream_t st);
 // dX rows of the tokens that count, from the splits' sums.
 cudaError_t launch_head_dx(int T, int d, int nsplit, int64_t Tp, float out_scale, const HeadRows& r, void* dX,
                            int num_sms, cudaStream_t st);

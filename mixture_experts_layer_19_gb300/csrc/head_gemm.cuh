@@ -227,9 +227,19 @@ struct HeadRow {
   int id0, id1;        // next two entries' vocabulary ids, INT_MAX past the list
   float p0, p1;
 
+  template <bool DIRECT>
   __device__ __forceinline__ void fetch_record(const HeadArgs& g, int64_t row, int na) {
     int4 q = make_int4(-1, 0, 0, 0);
-    if (row < na) q = __ldg(g.rec + row);
+    if (DIRECT && !g.n_active) {
+      if (row < na) {
+        const int64_t n = TEACHER ? (int64_t)__ldg(g.cnt + row)
+                          : g.ids64 ? __ldg(reinterpret_cast<const long long*>(g.labels) + row)
+                                    : (int64_t)__ldg(reinterpret_cast<const int*>(g.labels) + row);
+        if (TEACHER ? n > 0 : n >= 0 && n < g.V) q = make_int4((int)row, (int)n, 0, 0);
+      }
+    } else if (row < na) {
+      q = __ldg(g.rec + row);
+    }
     tok = q.x;
     cnt = q.y;
     rl = __int_as_float(q.z);
@@ -339,7 +349,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
   }
   WaitCtl wc{g.status, abort_flag, g.timeout_ns};
 
-  const int na = *g.n_active;
+  const int na = KIND == kHeadLse && !g.n_active ? g.T : *g.n_active;
   int MT, NT;
   const int64_t nwork = head_tiles<KIND, CG, AR>(g, na, MT, NT);
   const int bn = head_bn<AR>(g);
@@ -473,7 +483,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
       if (w0 < nwork) {
         const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w0);
         const int64_t vcol = g.v0 + t.col0 + h * half;
-        nxt.fetch_record(g, t.row0 + rank * kHBM + 32 * q + lane, na);
+        nxt.template fetch_record<KIND == kHeadLse>(g, t.row0 + rank * kHBM + 32 * q + lane, na);
         nxt.find_first(g, vcol);
         nxt.fetch_entries(g, vcol);
       }
@@ -492,7 +502,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         if (more) {
           const HeadTile n = head_tile<KIND, CG, AR>(g, na, MT, NT, w + wstep);
           nvcol = g.v0 + n.col0 + h * half;
-          nxt.fetch_record(g, n.row0 + rank * kHBM + 32 * q + lane, na);
+          nxt.template fetch_record<KIND == kHeadLse>(g, n.row0 + rank * kHBM + 32 * q + lane, na);
         }
         const int64_t left = min((int64_t)half, g.vlen - colh);   // its columns inside the vocabulary
         const int last = (int)vcol + half;                        // ids below it are this block's

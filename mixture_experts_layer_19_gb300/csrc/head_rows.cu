@@ -265,16 +265,21 @@ __device__ __forceinline__ void join(float& m, float& s, float om, float os) {
 // loss.  Four tokens per block (their pairs share a 32-byte sector): each
 // thread joins every 8 * warps-th pair, then threads and warps join in
 // a fixed order; one warp per token then adds up the target entries.
-__global__ void __launch_bounds__(1024) head_loss_kernel(int T, int K, int np, int64_t Tp, float temperature,
-                                                         int distill, HeadRows r, float* loss, float* lse) {
+__global__ void __launch_bounds__(1024) head_loss_kernel(const void* labels, int ids64, int T, int64_t V, int K, int np,
+                                                         int64_t Tp, float temperature, int distill, HeadRows r,
+                                                         float* loss, float* lse) {
   __shared__ float sm[4][32], ss[4][32];
   pdl_wait();
   pdl_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int t0 = blockIdx.x * 4;
+  auto row_of = [&](int t) {             // the row of a token that counts, else -1
+    if (r.inv) return r.inv[t];
+    return row_counts(labels, ids64, nullptr, V, r, t) ? t : -1;
+  };
   {
     const int t = t0 + (lane & 3);
-    const int row = t < T ? r.inv[t] : -1;
+    const int row = t < T ? row_of(t) : -1;
     float m = -CUDART_INF_F, s = 0.0f;
     if (row >= 0) {
       const float2* src = r.part + row;
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(int T, int K, int np, i
   __syncthreads();
   const int t = t0 + warp;
   if (warp >= 4 || t >= T) return;
-  const int row = r.inv[t];
+  const int row = row_of(t);
   if (row < 0) {
     if (lane == 0) {
       loss[t] = 0.0f;
@@ -384,11 +389,12 @@ cudaError_t launch_head_prep(const void* labels, bool ids64, const float* dloss,
                     reinterpret_cast<const uint4*>(X), d / 8, r, reinterpret_cast<uint4*>(dX));
 }
 
-cudaError_t launch_head_loss(int T, int K, int np, int64_t Tp, float temperature, bool distill, const HeadRows& r,
-                             float* loss, float* lse, cudaStream_t st) {
+cudaError_t launch_head_loss(const void* labels, bool ids64, int T, int64_t V, int K, int np, int64_t Tp,
+                             float temperature, bool distill, const HeadRows& r, float* loss, float* lse,
+                             cudaStream_t st) {
   // few blocks: more threads each
-  return launch_pdl(head_loss_kernel, dim3((T + 3) / 4), dim3(T <= 1024 ? 1024 : 256), 0, st, 1, T, K, np, Tp, temperature,
-                    (int)distill, r, loss, lse);
+  return launch_pdl(head_loss_kernel, dim3((T + 3) / 4), dim3(T <= 1024 ? 1024 : 256), 0, st, 1, labels, (int)ids64, T,
+                    V, K, np, Tp, temperature, (int)distill, r, loss, lse);
 }
 
 cudaError_t launch_head_dx(int T, int d, int nsplit, int64_t Tp, float out_scale, const HeadRows& r, void* dX,
