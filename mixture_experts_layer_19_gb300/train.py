@@ -12,7 +12,8 @@ Each operator comes as a pair of plain functions (``*_forward``,
 Losses are per token (fp32 [T]); reduce them as the training loop wants.
 Argument marshalling only: the kernels are libmoe.so's, and the formulas and
 error rules are those of include/moe.h.  Workspace comes from torch's caching
-allocator for each call, on the stream the call runs on.  Tensors are
+allocator for each call, on the stream the call runs on; a step can be
+captured in a CUDA graph after one call outside the capture.  Tensors are
 contiguous CUDA tensors, 16-byte aligned; ValueError says what is wrong with
 an argument before anything is enqueued.
 """
