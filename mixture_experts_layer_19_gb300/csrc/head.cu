@@ -100,7 +100,7 @@ struct Layout {
   int64_t Tp, piece, ldl;   // padded rows, columns of one piece, leading dimension of the D piece
   int K, nsplit;
   bool pair_z, pair_x, pair_w;   // CTA pairs for the logits, dX and dW products
-  int arows, bn;            // rows of A per CTA and columns of a tile in the logits products
+  int arows, bn;            // rows of A per CTA (without pairs), columns of a tile in the logits products
   bool sums;                // dX needs the fp32 sums (several pieces or splits)
   int64_t blocks;           // blocks of 128 vocabulary columns
   size_t counts, scale, rec, inv, ids, probs, first, cnt, plogp, xc, part, zt, dl, acc, total;
@@ -173,7 +173,7 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
   // SMs fetch (64 x 4096 x 8192 backward: 67.7 us against 60.2; 224 columns for 32768
   // entries, 147 tiles instead of 128, gained nothing).
   if (c.T <= 128) L.pair_z = false;
-  L.arows = L.pair_z || c.T > 64 ? 128 : c.T > 16 ? 64 : 16;
+  L.arows = c.T > 64 ? 128 : c.T > 16 ? 64 : 16;
   L.bn = L.arows < 128 ? (int)std::min<int64_t>(kHeadBN, up(ceil_div(zcols, sms), 64)) : kHeadBN;
   size_t o = 0;
   auto take = [&o](size_t bytes) {
@@ -319,7 +319,8 @@ moe_status_t run_head(const HeadCall& h, bool distill, bool backward) {
     ax = a;
     ax.nsplit = L.nsplit;
     ax.acc = r.acc;
-    ok = ok && map_k(&ax.mapA0, r.dl, L.ldl, L.Tp, L.ldl, 128) && map_k(&ax.mapB0, h.W, c.d, c.V, c.d, 64);
+    ok = ok && map_k(&ax.mapA0, r.dl, L.ldl, L.Tp, L.ldl, L.pair_x ? 128 : L.arows) &&
+         map_k(&ax.mapB0, h.W, c.d, c.V, c.d, 64);
     aw = a;
     aw.dW = static_cast<__nv_bfloat16*>(h.dW);
     aw.beside = h.dX != nullptr;

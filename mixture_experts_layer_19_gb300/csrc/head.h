@@ -60,7 +60,7 @@ struct HeadArgs {
 
 cudaError_t head_gemm_prepare();
 // pair: two CTAs work on one 256-row tile (cta_group::2); otherwise one CTA on 128 rows.
-// arows (kHeadLse, kHeadDl without pairs): rows of A per tile, 16, 64 or 128.
+// arows (without pairs, not kHeadDW): rows of A per tile, 16, 64 or 128.
 cudaError_t head_gemm_launch(int kind, bool pair, int arows, const HeadArgs& a, int grid, cudaStream_t st);
 cudaError_t head_gemm_max_pairs(int* pairs);
 

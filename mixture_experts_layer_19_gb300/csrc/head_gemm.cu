@@ -49,6 +49,8 @@ cudaError_t head_gemm_prepare() {
   cudaError_t e = prepare_logits<kHeadLse>();
   if (e == cudaSuccess) e = prepare_logits<kHeadDl>();
   if (e == cudaSuccess) e = prepare_one<kHeadDX, 1, false>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDX, 1, false, 16>();
+  if (e == cudaSuccess) e = prepare_one<kHeadDX, 1, false, 64>();
   if (e == cudaSuccess) e = prepare_one<kHeadDX, 2, false>();
   if (e == cudaSuccess) e = prepare_one<kHeadDW, 1, false>();
   if (e == cudaSuccess) e = prepare_one<kHeadDW, 2, false>();
@@ -59,7 +61,11 @@ cudaError_t head_gemm_launch(int kind, bool pair, int arows, const HeadArgs& a, 
   switch (kind) {
     case kHeadLse: return launch_logits<kHeadLse>(pair, arows, a, grid, st);
     case kHeadDl: return launch_logits<kHeadDl>(pair, arows, a, grid, st);
-    case kHeadDX: return pair ? launch_one<kHeadDX, 2, false>(a, grid, st) : launch_one<kHeadDX, 1, false>(a, grid, st);
+    case kHeadDX:
+      if (pair) return launch_one<kHeadDX, 2, false>(a, grid, st);
+      if (arows == 16) return launch_one<kHeadDX, 1, false, 16>(a, grid, st);
+      if (arows == 64) return launch_one<kHeadDX, 1, false, 64>(a, grid, st);
+      return launch_one<kHeadDX, 1, false>(a, grid, st);
     default: return pair ? launch_one<kHeadDW, 2, false>(a, grid, st) : launch_one<kHeadDW, 1, false>(a, grid, st);
   }
 }

@@ -47,10 +47,12 @@ constexpr int kLseChunkFew = 8;              // of up to 64 tokens (512), whose 
 // AR rows of A are fetched per CTA: 128, or 16 or 64 when the call has no more
 // tokens.  The product still covers 128 rows -- those past AR read whatever
 // follows in shared memory, and no one reads their results -- but the stages get
-// smaller, and more of W is on its way, which is what a call of few tokens waits for.
+// smaller, and more of W is on its way, which is what a call of few tokens waits
+// for.  Epilogue warps of rows past 64 then only hand the accumulator back.  In dX:
+// backward of 64 tokens, 2048 x 32768, 90.3 us with 128 rows of D per stage, 86.7 with 64.
 template <int KIND, int CG, int AR>
 struct HeadTraits {
-  static_assert(AR == kHBM || (CG == 1 && KIND <= kHeadDl));
+  static_assert(AR == kHBM || (CG == 1 && KIND <= kHeadDX));
   static constexpr bool a_mn = KIND == kHeadDW;
   static constexpr bool b_mn = KIND == kHeadDX || KIND == kHeadDW;
   static constexpr int a_bytes = AR * kHBK * 2;               // 16 KB for 128 rows
@@ -59,7 +61,8 @@ struct HeadTraits {
   static constexpr int stage_bytes = a_bytes + b_bytes;
   // staging per epilogue warp: 32 rows of 128 bytes
   static constexpr int staging = KIND == kHeadLse ? 0 : 4096;
-  static constexpr int spare = kHeadEpiWarps * staging + 1024 + 256;
+  static constexpr int staging_warps = AR == kHBM ? kHeadEpiWarps : kHeadEpiWarps / 2;
+  static constexpr int spare = staging_warps * staging + 1024 + 256;
   static constexpr int stages = AR == kHBM ? (CG == 2 ? 6 : 4) : (232448 - spare) / stage_bytes;
   static constexpr int smem_bytes = stages * stage_bytes + spare;
 };
@@ -72,10 +75,11 @@ struct HeadTile {
 };
 
 // Columns of a tile: 256; up to 64 tokens' logits products take what the call
-// says (64, 128, 192 or 256).
-template <int AR>
+// says (64, 128, 192 or 256).  dX's tiles stay 256 wide: its copies of W are whole
+// groups of four 64-column boxes, which the stage's byte count has to match.
+template <int KIND, int AR>
 __device__ __forceinline__ int head_bn(const HeadArgs& g) {
-  return AR == kHBM ? kHeadBN : g.bn;
+  return AR == kHBM || KIND > kHeadDl ? kHeadBN : g.bn;
 }
 
 template <int KIND, int CG, int AR>
@@ -83,7 +87,7 @@ __device__ __forceinline__ int64_t head_tiles(const HeadArgs& g, int na, int& MT
   constexpr int TM = kHBM * CG;
   const int64_t mrows = KIND == kHeadDW ? g.vlen : na;
   const int64_t ncols = KIND <= kHeadDl ? g.vlen : g.d;
-  const int bn = head_bn<AR>(g);
+  const int bn = head_bn<KIND, AR>(g);
   MT = (int)((mrows + TM - 1) / TM);
   NT = (int)((ncols + bn - 1) / bn);
   return (int64_t)MT * NT * (KIND == kHeadDX ? g.nsplit : 1);
@@ -107,7 +111,7 @@ __device__ __forceinline__ HeadTile head_tile(const HeadArgs& g, int na, int MT,
     mt = local - nt * MT;
   }
   t.row0 = mt * (kHBM * CG);
-  t.col0 = nt * head_bn<AR>(g);
+  t.col0 = nt * head_bn<KIND, AR>(g);
   t.kb0 = 0;
   if (KIND == kHeadDX) {
     const int nkb = (int)((g.vlen + kHBK - 1) / kHBK);
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stage_base = smem;
   uint8_t* staging_base = smem + kSt * TR::stage_bytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging_base + kHeadEpiWarps * TR::staging);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging_base + TR::staging_warps * TR::staging);
   uint64_t* full = bars;                 // used in the leader CTA
   uint64_t* empty = bars + kSt;
   uint64_t* tfull = bars + 2 * kSt;
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
   const int na = KIND == kHeadLse && !g.n_active ? g.T : *g.n_active;
   int MT, NT;
   const int64_t nwork = head_tiles<KIND, CG, AR>(g, na, MT, NT);
-  const int bn = head_bn<AR>(g);
+  const int bn = head_bn<KIND, AR>(g);
   const int64_t w0 = blockIdx.x / CG;
   const int64_t wstep = gridDim.x / CG;
 
@@ -463,7 +467,8 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;                 // TMEM lane quadrant of this warp
     const int h = (warp - 2) >> 2;          // column half
-    uint8_t* stg = staging_base + (warp - 2) * TR::staging;
+    const bool idle = AR != kHBM && q >= 2; // rows past 64 of a call with no more
+    uint8_t* stg = staging_base + (AR == kHBM ? warp - 2 : 2 * h + (q & 1)) * TR::staging;
     uint32_t acc = 0, aph = 0;
     const float c2 = g.inv_temp * 1.4426950408889634f;   // logits to base-2 exponents
     auto release = [&](uint32_t a) {
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     [[maybe_unused]] HeadRow<TEACHER> cur, nxt;
     const int half = bn / 2;                                      // columns of a warp: 32, 64, 96 or 128
     if constexpr (KIND <= kHeadDl) {
-      if (w0 < nwork) {
+      if (w0 < nwork && !idle) {
         const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w0);
         const int64_t vcol = g.v0 + t.col0 + h * half;
         nxt.template fetch_record<KIND == kHeadLse>(g, t.row0 + rank * kHBM + 32 * q + lane, na);
@@ -490,6 +495,20 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
     }
     for (int64_t w = w0; w < nwork; w += wstep) {
       const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
+      if (idle) {
+        bool ok = true;
+        const int phases = t.nkb > 0 ? head_phases<KIND, AR>(t.nkb) : 0;
+        for (int p = 0; p < phases && ok; ++p) {
+          ok = mbar_wait(&tfull[acc], aph, wc);
+          if (!ok) break;
+          tc_fence_after();
+          release(acc);
+          acc ^= 1;
+          if (acc == 0) aph ^= 1;
+        }
+        if (!ok) break;
+        continue;
+      }
       const int64_t rowq = t.row0 + rank * kHBM + 32 * q;         // the warp's first row
       const int64_t row = rowq + lane;                            // this lane's row
       const int64_t colh = t.col0 + h * half;                     // the warp's first column
