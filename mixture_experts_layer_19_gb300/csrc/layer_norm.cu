@@ -913,11 +913,15 @@ int64_t bwd_blocks(int64_t rows, int threads, int sms) {
 }
 int64_t long_slices(int64_t rows) { return std::min<int64_t>(rows, 32); }
 
-// A launch's dynamic shared memory past the 48 KB that need no leave.
+// Leave for a launch's dynamic shared memory.  What needs none is 48 KB with the
+// kernel's static part, up to 2.3 KB here.  Always the same maximum (with the static
+// part below the 227 KB of a block): one call never lowers what another, on some
+// other thread, is about to launch with.
+constexpr int kMaxSmem = 224 << 10;
 template <class K>
 cudaError_t allow_smem(K kernel, int bytes) {
-  if (bytes <= 48 << 10) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (bytes <= 44 << 10) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
 }
 
 template <class XT, class WT, int VW, int VPT>

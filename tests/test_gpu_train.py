@@ -119,6 +119,35 @@ def test_layer_norm_many_rows(train, rows, d, xt):
     check_ln(train, *ln_inputs(rows, d, xt, torch.float32, seed=7))
 
 
+# Rows whose shared memory comes to just 48 KB, of which the static part leaves a
+# launch less without leave; the kernels of wider rows would ask for it first.
+LN_48_KB = [(1830, 6144, torch.bfloat16), (9, 2048, torch.float32), (5, 2435, torch.bfloat16), (5, 2030, torch.float32)]
+
+
+def ln_first_calls(queue):
+    from mixture_experts_layer_19_gb300 import train
+    failed = []
+    for rows, d, xt in LN_48_KB:
+        try:
+            check_ln(train, *ln_inputs(rows, d, xt, torch.float32, seed=d))
+        except Exception as e:
+            failed.append(f"{rows} x {d} {xt}: {e}")
+    queue.put(failed)
+
+
+def test_layer_norm_near_48_kb_in_a_new_process():
+    import torch.multiprocessing as mp
+    ctx = mp.get_context("spawn")
+    queue = ctx.Queue()
+    child = ctx.Process(target=ln_first_calls, args=(queue,))
+    child.start()
+    try:
+        assert queue.get(timeout=240) == []
+    finally:
+        child.join(60)
+    assert child.exitcode == 0
+
+
 def test_layer_norm_mean_far_from_zero_and_no_bias(train):
     """A difference of sums would lose the variance here: the mean is 300 spreads away."""
     x, w, _, dy = ln_inputs(40, 1024, torch.float32, torch.float32, seed=3, shift=600.0)
