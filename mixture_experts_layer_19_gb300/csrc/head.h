@@ -31,7 +31,7 @@ struct HeadArgs {
   int ids64;
   int64_t V;
   const int4* rec;           // [Tp] of each compact row: token, label (or teacher entries in use), and, as float
-                             //   bits for kHeadDl, log-sum-exp in base 2 and upstream gradient / *scale
+                             //   bits for kHeadDl, log-sum-exp and upstream gradient / *scale
   const int32_t* ids;        // distillation: [T, K] entries in use of each token, ids ascending
   const float* probs;        // [T, K] their probabilities
   const uint16_t* first;     // [T, blocks] first entry at or past vocabulary column 128 * block; NULL: labels

@@ -9,8 +9,9 @@
 //   kHeadDX   D . W      (K = vocabulary piece) into fp32 sums
 //   kHeadDW   D^T . X    (K = tokens), one bf16 rounding
 //
-// Roles per CTA (320 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA
-// issuer, warps 2..9 epilogue (two per TMEM lane quadrant, 128 columns each).
+// Roles per CTA (320 threads, 384 with two idle warps): warp 0 TMA producer, warp 1
+// TMEM owner and MMA issuer, the last eight warps epilogue (two per TMEM lane
+// quadrant, 128 columns each).
 // CG = 1: one CTA computes a 128 x 256 tile.  CG = 2: a pair of CTAs computes
 // 256 x 256; each holds its 128 rows of A and half of B's 256 columns, so an
 // SM fetches 32 KB instead of 48 KB per 64-deep slice of K.
@@ -27,9 +28,14 @@
 //
 // The tensor cores add into fp32 accumulators with truncation, which pulls a
 // 7168-long dot product towards zero by about 7e-6 of its value (measured
-// against 64 bits).  The loss is a difference of logits, so kHeadLse ends an
-// accumulator every kLseChunk slices of K and adds the parts in registers,
-// rounded to nearest.  The gradients are rounded to bf16 and do not need it.
+// against 64 bits).  The loss is a difference of logits, and D the difference of
+// the softmax and its target, so both logits products end an accumulator every
+// kLogitsChunk slices of K and add the parts in registers, rounded to nearest.
+// The runs are the same in both directions: D subtracts from the very logits that
+// the log-sum-exp was taken of.  With D in one run over K, gradients of tokens
+// predicted with 0.997 to 0.9995 at width 7168, from logits of 40, were off by 40%
+// (norm of a row of dX); in parts they are off by 0.24%.  The sums dX and dW, of
+// entries of D that were rounded to bf16, do not need it.
 #pragma once
 #include "head.h"
 #include "pdl.cuh"
@@ -39,10 +45,19 @@ namespace moe {
 
 constexpr int kHBM = 128;                    // rows per CTA
 constexpr int kHBK = 64;                     // K slice (128 bytes of bf16)
-constexpr int kHeadThreads = 320;
 constexpr int kHeadEpiWarps = 8;
-constexpr int kLseChunk = 16;                // K slices per accumulator of kHeadLse (1024), and
-constexpr int kLseChunkFew = 8;              // of up to 64 tokens (512), whose epilogues have the time
+// Adding up a logit's parts takes 128 registers beside what the epilogue needs, and 320 threads get
+// 168 each: they spilled 160-220 bytes in kHeadLse.  The kernels with parts have two idle warps more,
+// so that the first four make a warpgroup that hands registers to the epilogue's two.
+constexpr int kLaunchRegs = 168, kFewRegs = 56, kEpiRegs = 224;
+template <int KIND, bool PARTS>
+constexpr bool head_regs = KIND == kHeadLse || (KIND == kHeadDl && PARTS);
+template <int KIND, bool PARTS>
+constexpr int head_threads = (head_regs<KIND, PARTS> ? 4 : 2) * 32 + kHeadEpiWarps * 32;
+static_assert(4 * kFewRegs + kHeadEpiWarps * kEpiRegs <= 12 * kLaunchRegs, "the shares come out of the launch's registers");
+constexpr int kLogitsChunk = 16;             // K slices per accumulator of the logits products (1024), and
+constexpr int kLogitsChunkFew = 8;           // of up to 64 tokens (512), whose epilogues have the time
+constexpr int logits_chunk(int arows) { return arows == kHBM ? kLogitsChunk : kLogitsChunkFew; }
 
 // AR rows of A are fetched per CTA: 128, or 16 or 64 when the call has no more
 // tokens.  The product still covers 128 rows -- those past AR read whatever
@@ -125,10 +140,9 @@ __device__ __forceinline__ HeadTile head_tile(const HeadArgs& g, int na, int MT,
 }
 
 // Accumulators (TMEM phases) of one tile.
-template <int KIND, int AR>
+template <int KIND, int AR, bool PARTS>
 __device__ __forceinline__ int head_phases(int nkb) {
-  constexpr int chunk = AR == kHBM ? kLseChunk : kLseChunkFew;
-  return KIND == kHeadLse ? (nkb + chunk - 1) / chunk : 1;
+  return KIND == kHeadLse || (KIND == kHeadDl && PARTS) ? (nkb + logits_chunk(AR) - 1) / logits_chunk(AR) : 1;
 }
 
 // ---------------------------------------------------------------- pair (cta_group::2) pieces
@@ -226,7 +240,7 @@ template <bool TEACHER>
 struct HeadRow {
   int tok;             // token, -1 past the rows that count
   int cnt;             // TEACHER: entries in use; else the label
-  float rl, gr;        // kHeadDl: log-sum-exp in base 2, upstream gradient over the common factor
+  float rl, gr;        // kHeadDl: log-sum-exp, upstream gradient over the common factor
   int e;               // next entry
   int id0, id1;        // next two entries' vocabulary ids, INT_MAX past the list
   float p0, p1;
@@ -295,8 +309,11 @@ __device__ __forceinline__ float pick32(const float* v, int col) {
   return (col & 16) ? t[2] : t[0];
 }
 
-template <int KIND, int CG, bool TEACHER, int AR>
-__global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid_constant__ HeadArgs g) {
+// PARTS (kHeadDl): a logit has several parts.  Widths with one (up to 1024, or 512 for up to 64 tokens) have
+// a kernel of their own, without the registers for more: distillation backward of 2048 tokens, 512 x
+// 32768, K = 64, 196 us against 204 with one kernel for all widths.
+template <int KIND, int CG, bool TEACHER, int AR, bool PARTS>
+__global__ void __launch_bounds__(head_threads<KIND, PARTS>, 1) head_gemm_kernel(const __grid_constant__ HeadArgs g) {
   using TR = HeadTraits<KIND, CG, AR>;
   constexpr int kSt = TR::stages;
   extern __shared__ uint8_t smem_raw[];
@@ -360,117 +377,125 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
   const int64_t w0 = blockIdx.x / CG;
   const int64_t wstep = gridDim.x / CG;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
-      fence_proxy_async_global();                       // the predecessors' plain stores, read by TMA below
-      const uint64_t pol = policy_evict_last();
-      const uint64_t pol_b = (KIND == kHeadLse || KIND == kHeadDX) && g.T <= kHBM * CG ? policy_evict_first() : pol;
-      const bool all = na == g.T;                       // no row skipped: X is read in place
-      const CUtensorMap* mA = (KIND <= kHeadDl && !all) ? &g.mapA1 : &g.mapA0;
-      const CUtensorMap* mB = (KIND == kHeadDW && !all) ? &g.mapB1 : &g.mapB0;
-      uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
-      bool ok = true;
-      for (int64_t w = w0; w < nwork && ok && !g.stall; w += wstep) {
-        const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
-        const int64_t arow = t.row0 + rank * kHBM;          // this CTA's rows of A
-        const int64_t bcol = t.col0 + rank * TR::b_rows;    // and columns of B
-        for (int kb = 0; kb < t.nkb; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1, wc)) { ok = false; break; }
-          if (leader) mbar_arrive_expect_tx(&full[s], TR::a_bytes * CG + bn * kHBK * 2);
-          uint8_t* sa = stage_base + s * TR::stage_bytes;
-          uint8_t* sb = sa + TR::a_bytes;
-          const int32_t k0 = (t.kb0 + kb) * kHBK;
-          const uint32_t bar_c = CG == 2 ? mapa_u32(smem_u32(&full[s]), 0) : 0;
-          auto load = [&](uint8_t* dst, const CUtensorMap* m, int64_t x, int64_t y, uint64_t pol) {
-            if constexpr (CG == 1) tma_load_2d(dst, m, (int32_t)x, (int32_t)y, &full[s], pol);
-            else tma_load_2d_pair(dst, m, (int32_t)x, (int32_t)y, bar_c, pol);
-          };
-          if (KIND == kHeadDW) {
-#pragma unroll
-            for (int j = 0; j < kHBM / 64; ++j) load(sa + j * 8192, mA, arow + j * 64, k0, pol);
-          } else {
-            load(sa, mA, k0, arow, pol);
-          }
-          if (KIND == kHeadDX || KIND == kHeadDW) {
-            const int64_t krow = (KIND == kHeadDX ? g.v0 : 0) + k0;
-#pragma unroll
-            for (int j = 0; j < TR::b_rows / 64; ++j) load(sb + j * 8192, mB, bcol + j * 64, krow, pol_b);
-          } else {
-            load(sb, mB, k0, g.v0 + bcol, pol_b);
-          }
-          issued |= 1u << s;
-          last_par = (last_par & ~(1u << s)) | (ph << s);
-          if (++s == kSt) { s = 0; ph ^= 1; }
-        }
-      }
-      if (!ok) {
-        // abort: give every issued copy time to land before the CTA may exit
-        // (the barriers are the leader's; its peer waits a fixed time)
-        const uint64_t t0 = globaltimer_ns();
-        if (leader) {
-          for (int st = 0; st < kSt; ++st) {
-            if (!(issued & (1u << st))) continue;
-            while (!mbar_try_wait(&full[st], (last_par >> st) & 1u))
-              if (globaltimer_ns() - t0 > 50000000ull) break;
-          }
-        } else {
-          while (globaltimer_ns() - t0 < 5000000ull) __nanosleep(1000);
-        }
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ------------------------------------------------------------ MMA issuer
-      const uint32_t idesc = idesc_bf16(kHBM * CG, bn, TR::a_mn ? 1 : 0, TR::b_mn ? 1 : 0);
-      uint32_t s = 0, ph = 0, acc = 0, aph = 0;
-      bool ok = true;
-      for (int64_t w = w0; w < nwork && ok; w += wstep) {
-        const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
-        if (t.nkb == 0) continue;
-        const int phases = head_phases<KIND, AR>(t.nkb);
-        for (int p = 0; p < phases && ok; ++p) {
-          const int k_lo = (int)((int64_t)t.nkb * p / phases), k_hi = (int)((int64_t)t.nkb * (p + 1) / phases);
-          if (!mbar_wait(&tempty[acc], aph ^ 1, wc)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t d_tmem = tmem_base + acc * kHeadBN;
-          for (int kb = k_lo; kb < k_hi; ++kb) {
-            if (!mbar_wait(&full[s], ph, wc)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t sa = smem_u32(stage_base + s * TR::stage_bytes);
-            const uint32_t sb = sa + TR::a_bytes;
-#pragma unroll
-            for (int kk = 0; kk < kHBK / 16; ++kk) {
-              const uint64_t ad =
-                  TR::a_mn ? sdesc_sw128(sa + kk * 2048, 8192, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024);
-              const uint64_t bd =
-                  TR::b_mn ? sdesc_sw128(sb + kk * 2048, 8192, 1024) : sdesc_sw128(sb + kk * 32, 16, 1024);
-              head_mma<CG>(d_tmem, ad, bd, idesc, (kb > k_lo || kk) ? 1u : 0u);
+  constexpr int kEpi0 = head_threads<KIND, PARTS> / 32 - kHeadEpiWarps;      // the epilogue's first warp
+  if (warp < kEpi0) {
+    if constexpr (head_regs<KIND, PARTS>) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if (warp == 0) {
+      if (lane == 0) {
+        // ------------------------------------------------------------ producer
+        fence_proxy_async_global();                       // the predecessors' plain stores, read by TMA below
+        const uint64_t pol = policy_evict_last();
+        const uint64_t pol_b = (KIND == kHeadLse || KIND == kHeadDX) && g.T <= kHBM * CG ? policy_evict_first() : pol;
+        const bool all = na == g.T;                       // no row skipped: X is read in place
+        const CUtensorMap* mA = (KIND <= kHeadDl && !all) ? &g.mapA1 : &g.mapA0;
+        const CUtensorMap* mB = (KIND == kHeadDW && !all) ? &g.mapB1 : &g.mapB0;
+        uint32_t s = 0, ph = 0, issued = 0, last_par = 0;
+        bool ok = true;
+        for (int64_t w = w0; w < nwork && ok && !g.stall; w += wstep) {
+          const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
+          const int64_t arow = t.row0 + rank * kHBM;          // this CTA's rows of A
+          const int64_t bcol = t.col0 + rank * TR::b_rows;    // and columns of B
+          for (int kb = 0; kb < t.nkb; ++kb) {
+            if (!mbar_wait(&empty[s], ph ^ 1, wc)) { ok = false; break; }
+            if (leader) mbar_arrive_expect_tx(&full[s], TR::a_bytes * CG + bn * kHBK * 2);
+            uint8_t* sa = stage_base + s * TR::stage_bytes;
+            uint8_t* sb = sa + TR::a_bytes;
+            const int32_t k0 = (t.kb0 + kb) * kHBK;
+            const uint32_t bar_c = CG == 2 ? mapa_u32(smem_u32(&full[s]), 0) : 0;
+            auto load = [&](uint8_t* dst, const CUtensorMap* m, int64_t x, int64_t y, uint64_t pol) {
+              if constexpr (CG == 1) tma_load_2d(dst, m, (int32_t)x, (int32_t)y, &full[s], pol);
+              else tma_load_2d_pair(dst, m, (int32_t)x, (int32_t)y, bar_c, pol);
+            };
+            if (KIND == kHeadDW) {
+  #pragma unroll
+              for (int j = 0; j < kHBM / 64; ++j) load(sa + j * 8192, mA, arow + j * 64, k0, pol);
+            } else {
+              load(sa, mA, k0, arow, pol);
             }
-            head_commit<CG>(&empty[s]);
+            if (KIND == kHeadDX || KIND == kHeadDW) {
+              const int64_t krow = (KIND == kHeadDX ? g.v0 : 0) + k0;
+  #pragma unroll
+              for (int j = 0; j < TR::b_rows / 64; ++j) load(sb + j * 8192, mB, bcol + j * 64, krow, pol_b);
+            } else {
+              load(sb, mB, k0, g.v0 + bcol, pol_b);
+            }
+            issued |= 1u << s;
+            last_par = (last_par & ~(1u << s)) | (ph << s);
             if (++s == kSt) { s = 0; ph ^= 1; }
           }
-          if (!ok) break;
-          head_commit<CG>(&tfull[acc]);
-          acc ^= 1;
-          if (acc == 0) aph ^= 1;
+        }
+        if (!ok) {
+          // abort: give every issued copy time to land before the CTA may exit
+          // (the barriers are the leader's; its peer waits a fixed time)
+          const uint64_t t0 = globaltimer_ns();
+          if (leader) {
+            for (int st = 0; st < kSt; ++st) {
+              if (!(issued & (1u << st))) continue;
+              while (!mbar_try_wait(&full[st], (last_par >> st) & 1u))
+                if (globaltimer_ns() - t0 > 50000000ull) break;
+            }
+          } else {
+            while (globaltimer_ns() - t0 < 5000000ull) __nanosleep(1000);
+          }
         }
       }
-      if (!ok) {  // abort: let the products in flight finish before TMEM is freed
-        head_commit<CG>(drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(drain, 0))
-          if (globaltimer_ns() - t0 > 50000000ull) break;
+    } else if (warp == 1) {
+      if (lane == 0 && leader) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t idesc = idesc_bf16(kHBM * CG, bn, TR::a_mn ? 1 : 0, TR::b_mn ? 1 : 0);
+        uint32_t s = 0, ph = 0, acc = 0, aph = 0;
+        bool ok = true;
+        for (int64_t w = w0; w < nwork && ok; w += wstep) {
+          const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
+          if (t.nkb == 0) continue;
+          const int phases = head_phases<KIND, AR, PARTS>(t.nkb);
+          const int len = t.nkb / phases, longer = t.nkb - len * phases;
+          int k_hi = 0;
+          for (int p = 0; p < phases && ok; ++p) {
+            const int k_lo = k_hi;
+            k_hi += len + (p < longer ? 1 : 0);
+            if (!mbar_wait(&tempty[acc], aph ^ 1, wc)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + acc * kHeadBN;
+            for (int kb = k_lo; kb < k_hi; ++kb) {
+              if (!mbar_wait(&full[s], ph, wc)) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t sa = smem_u32(stage_base + s * TR::stage_bytes);
+              const uint32_t sb = sa + TR::a_bytes;
+  #pragma unroll
+              for (int kk = 0; kk < kHBK / 16; ++kk) {
+                const uint64_t ad =
+                    TR::a_mn ? sdesc_sw128(sa + kk * 2048, 8192, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024);
+                const uint64_t bd =
+                    TR::b_mn ? sdesc_sw128(sb + kk * 2048, 8192, 1024) : sdesc_sw128(sb + kk * 32, 16, 1024);
+                head_mma<CG>(d_tmem, ad, bd, idesc, (kb > k_lo || kk) ? 1u : 0u);
+              }
+              head_commit<CG>(&empty[s]);
+              if (++s == kSt) { s = 0; ph ^= 1; }
+            }
+            if (!ok) break;
+            head_commit<CG>(&tfull[acc]);
+            acc ^= 1;
+            if (acc == 0) aph ^= 1;
+          }
+        }
+        if (!ok) {  // abort: let the products in flight finish before TMEM is freed
+          head_commit<CG>(drain);
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(drain, 0))
+            if (globaltimer_ns() - t0 > 50000000ull) break;
+        }
       }
     }
   } else {
     // -------------------------------------------------------------- epilogue
+    if constexpr (head_regs<KIND, PARTS>) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int q = warp & 3;                 // TMEM lane quadrant of this warp
-    const int h = (warp - 2) >> 2;          // column half
+    const int h = (warp - kEpi0) >> 2;      // column half
     const bool idle = AR != kHBM && q >= 2; // rows past 64 of a call with no more
-    uint8_t* stg = staging_base + (AR == kHBM ? warp - 2 : 2 * h + (q & 1)) * TR::staging;
+    uint8_t* stg = staging_base + (AR == kHBM ? warp - kEpi0 : 2 * h + (q & 1)) * TR::staging;
     uint32_t acc = 0, aph = 0;
-    const float c2 = g.inv_temp * 1.4426950408889634f;   // logits to base-2 exponents
+    [[maybe_unused]] const float c2 = g.inv_temp * 1.4426950408889634f;   // logits to base-2 exponents
     auto release = [&](uint32_t a) {
       tc_fence_before();
       __syncwarp();
@@ -497,7 +522,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
       const HeadTile t = head_tile<KIND, CG, AR>(g, na, MT, NT, w);
       if (idle) {
         bool ok = true;
-        const int phases = t.nkb > 0 ? head_phases<KIND, AR>(t.nkb) : 0;
+        const int phases = t.nkb > 0 ? head_phases<KIND, AR, PARTS>(t.nkb) : 0;
         for (int p = 0; p < phases && ok; ++p) {
           ok = mbar_wait(&tfull[acc], aph, wc);
           if (!ok) break;
@@ -525,33 +550,35 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
         }
         const int64_t left = min((int64_t)half, g.vlen - colh);   // its columns inside the vocabulary
         const int last = (int)vcol + half;                        // ids below it are this block's
-        if constexpr (KIND == kHeadLse) {
-          float z[128] = {};
-          const int phases = head_phases<KIND, AR>(t.nkb);
-          bool ok = true;
-          for (int p = 0; p < phases; ++p) {
-            if (!mbar_wait(&tfull[acc], aph, wc)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * half;
+        // the row's 128 logits; kHeadDl takes the last part as it goes, 32 columns at a time
+        float z[128] = {};
+        const int phases = head_phases<KIND, AR, PARTS>(t.nkb);
+        const int whole = KIND == kHeadLse ? phases : phases - 1;   // 0 without PARTS
+        bool ok = true;
+        for (int p = 0; p < whole; ++p) {
+          if (!mbar_wait(&tfull[acc], aph, wc)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t tb = tmem_base + lane_off + acc * kHeadBN + h * half;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (c * 32 >= half) break;
-              uint32_t r[32];
-              tmem_ld32(tb + c * 32, r);
-              tmem_ld_wait();
-              if (p == 0) {
+          for (int c = 0; c < 4; ++c) {
+            if (c * 32 >= half) break;
+            uint32_t r[32];
+            tmem_ld32(tb + c * 32, r);
+            tmem_ld_wait();
+            if (p == 0) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[c * 32 + i] = __uint_as_float(r[i]);
-              } else {
+              for (int i = 0; i < 32; ++i) z[c * 32 + i] = __uint_as_float(r[i]);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[c * 32 + i] += __uint_as_float(r[i]);
-              }
+              for (int i = 0; i < 32; ++i) z[c * 32 + i] += __uint_as_float(r[i]);
             }
-            release(acc);
-            acc ^= 1;
-            if (acc == 0) aph ^= 1;
           }
-          if (!ok) break;
+          release(acc);
+          acc ^= 1;
+          if (acc == 0) aph ^= 1;
+        }
+        if (!ok) break;
+        if constexpr (KIND == kHeadLse) {
           if (more) nxt.find_first(g, nvcol);
           // logits at this row's target entries inside these 128 columns
           while (__any_sync(0xffffffffu, cur.id0 < last)) {
@@ -576,11 +603,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
           for (int i = 4; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], z[i]);
           const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           const float mb = m == -INFINITY ? 0.0f : m * c2;        // a block without columns sums to 0
+          const float md = m == -INFINITY ? 0.0f : fmaf(m, c2, -mb);   // the sum is taken about m, not about mb
           float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int i = 0; i < 128; ++i) s4[i & 3] += ex2_approx(fmaf(z[i], c2, -mb));
           g.part[(2 * (t.col0 / bn) + h) * g.Tp + row] =
-              make_float2(m * g.inv_temp, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+              make_float2(m * g.inv_temp, ((s4[0] + s4[1]) + (s4[2] + s4[3])) * ex2_approx(-md));
         } else {
           if (!mbar_wait(&tfull[acc], aph, wc)) break;
           tc_fence_after();
@@ -594,9 +622,16 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_gemm_kernel(const __grid
             tmem_ld_wait();
             float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = ex2_approx(fmaf(__uint_as_float(r[i]), c2, -cur.rl));
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            if (whole > 0) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = z[c * 32 + i] + v[i];
+            }
             if (c * 32 + 32 < half) tmem_ld32(tb + (c + 1) * 32, r);
             else release(acc);
+            // the difference first: near the log-sum-exp it is exact, and its size sets the rounding
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = ex2_approx(fmaf(v[i], g.inv_temp, -cur.rl) * 1.4426950408889634f);
             const int until = (int)vcol + c * 32 + 32;
             while (__any_sync(0xffffffffu, cur.id0 < until)) {
               const bool hit = cur.id0 < until;

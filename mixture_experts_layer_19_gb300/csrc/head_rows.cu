@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(256) head_prep_kernel(const void* labels, int 
     const int rows = min(256, t1 - base);
     if (on) {
       r.rec[before + at] = make_int4(t, labels ? (int)load_id(labels, ids64, t) : r.cnt[t],
-                                     __float_as_int(dloss ? lse[t] * 1.4426950408889634f : 0.0f),
+                                     __float_as_int(dloss ? lse[t] : 0.0f),
                                      __float_as_int(dloss ? dloss[t] / scale : 0.0f));
       s_on[at] = t;
     } else if (t < t1) {
