@@ -15,7 +15,8 @@ error rules are those of include/moe.h.  Workspace comes from torch's caching
 allocator for each call, on the stream the call runs on; a step can be
 captured in a CUDA graph after one call outside the capture.  Tensors are
 contiguous CUDA tensors, 16-byte aligned; ValueError says what is wrong with
-an argument before anything is enqueued.
+an argument before anything is enqueued.  The differentiable functions and the
+modules first copy activations, gradients and norm weights laid out otherwise.
 """
 from __future__ import annotations
 
@@ -57,6 +58,15 @@ def _ptr(t: torch.Tensor, name: str, index: int, align: int = 16) -> int:
             raise ValueError(f"{name}: must be contiguous")
         raise ValueError(f"{name}: must be {align}-byte aligned")
     return p
+
+
+def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """t as the library takes it: contiguous, 16-byte aligned, copied where it is not.  The gradient of a
+    part of a tensor, as cat and split hand it back, is a contiguous view that starts anywhere."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
 
 
 def _elsewhere(index: int, stream: Optional[torch.cuda.Stream]):
@@ -188,7 +198,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, need_dx: bool = True, need_dw
 class _LayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
-        x = x.contiguous()
+        x, weight, bias = _dense(x), _dense(weight), _dense(bias)
         y, mean, rstd = layer_norm_forward(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
         return y
@@ -198,7 +208,7 @@ class _LayerNormFunction(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dx, dw, db = layer_norm_backward(dy.contiguous(), x, weight, mean, rstd, need_dx=need[0],
+        dx, dw, db = layer_norm_backward(_dense(dy), x, weight, mean, rstd, need_dx=need[0],
                                          need_dweight=need[1], need_dbias=need[2])
         return dx, dw, db, None
 
@@ -372,7 +382,7 @@ def distill_backward(dloss, X, W, teacher_logits, teacher_ids, lse, temperature:
 class _CrossEntropyFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, labels):
-        X = X.contiguous()
+        X = _dense(X)
         loss, lse = cross_entropy_forward(X, W, labels)
         ctx.save_for_backward(X, W, labels, lse)
         return loss
@@ -389,7 +399,7 @@ class _CrossEntropyFunction(torch.autograd.Function):
 class _DistillFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, teacher_logits, teacher_ids, temperature):
-        X = X.contiguous()
+        X = _dense(X)
         loss, lse = distill_forward(X, W, teacher_logits, teacher_ids, temperature)
         ctx.temperature = temperature
         ctx.save_for_backward(X, W, teacher_logits, teacher_ids, lse)
