@@ -16,7 +16,8 @@ allocator for each call, on the stream the call runs on; a step can be
 captured in a CUDA graph after one call outside the capture.  Tensors are
 contiguous CUDA tensors, 16-byte aligned; ValueError says what is wrong with
 an argument before anything is enqueued.  The differentiable functions and the
-modules first copy activations, gradients and norm weights laid out otherwise.
+modules first copy activations, targets, gradients and norm weights laid out
+otherwise.
 """
 from __future__ import annotations
 
@@ -382,7 +383,7 @@ def distill_backward(dloss, X, W, teacher_logits, teacher_ids, lse, temperature:
 class _CrossEntropyFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, labels):
-        X = _dense(X)
+        X, labels = _dense(X), labels.contiguous()
         loss, lse = cross_entropy_forward(X, W, labels)
         ctx.save_for_backward(X, W, labels, lse)
         return loss
@@ -399,7 +400,7 @@ class _CrossEntropyFunction(torch.autograd.Function):
 class _DistillFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, teacher_logits, teacher_ids, temperature):
-        X = _dense(X)
+        X, teacher_logits, teacher_ids = _dense(X), teacher_logits.contiguous(), teacher_ids.contiguous()
         loss, lse = distill_forward(X, W, teacher_logits, teacher_ids, temperature)
         ctx.temperature = temperature
         ctx.save_for_backward(X, W, teacher_logits, teacher_ids, lse)
@@ -414,14 +415,32 @@ class _DistillFunction(torch.autograd.Function):
         return dX, dW, None, None, None
 
 
+def _rows(X, **targets):
+    """X [..., d] and what each of its rows is trained on, as matrices of that many rows."""
+    lead = X.shape[:-1]
+    for name, t in targets.items():
+        if t.shape[:len(lead)] != lead:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected one that starts with {tuple(lead)}")
+    n = lead.numel()
+    return [t.reshape(n, *t.shape[len(lead):]) for t in (X, *targets.values())]
+
+
 def linear_cross_entropy(X, W, labels) -> torch.Tensor:
-    """Differentiable per-token loss fp32 [T] of the head W [V, d] on X [T, d]."""
-    return _CrossEntropyFunction.apply(X, W, labels)
+    """Differentiable per-token loss fp32 [...] of the head W [V, d] on X [..., d] with labels [...]."""
+    if X.dim() == 2:
+        return _CrossEntropyFunction.apply(X, W, labels)
+    rows, labels = _rows(X, labels=labels)
+    return _CrossEntropyFunction.apply(rows, W, labels).view(X.shape[:-1])
 
 
 def linear_distillation(X, W, teacher_logits, teacher_ids, temperature: float = 1.0) -> torch.Tensor:
-    """Differentiable per-token distillation loss fp32 [T] (the teacher gets no gradient)."""
-    return _DistillFunction.apply(X, W, teacher_logits.detach(), teacher_ids, temperature)
+    """Differentiable per-token distillation loss fp32 [...] of X [..., d] from teacher logits and ids
+    [..., K] (the teacher gets no gradient)."""
+    teacher_logits = teacher_logits.detach()
+    if X.dim() == 2:
+        return _DistillFunction.apply(X, W, teacher_logits, teacher_ids, temperature)
+    rows, teacher_logits, teacher_ids = _rows(X, teacher_logits=teacher_logits, teacher_ids=teacher_ids)
+    return _DistillFunction.apply(rows, W, teacher_logits, teacher_ids, temperature).view(X.shape[:-1])
 
 
 class LMHead(torch.nn.Module):

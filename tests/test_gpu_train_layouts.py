@@ -74,3 +74,48 @@ def test_head_activations_that_start_anywhere(train):
         assert torch.equal(call(got), call(ref))
         call(got).sum().backward()
         assert torch.equal(got.grad, ref.grad)
+
+
+def test_strided_targets(train):
+    """Labels, teacher logits and ids as columns, transposes and reversed views of larger tensors."""
+    T, d, V, K = 40, 64, 300, 4
+    g = gen(4)
+    X = torch.randn((T, d), generator=g, device=DEV).to(torch.bfloat16)
+    W = torch.randn((V, d), generator=g, device=DEV).to(torch.bfloat16)
+    batch = torch.randint(0, V, (T, 2), generator=g, device=DEV)
+    u, ids = torch.randn((K, T), generator=g, device=DEV), torch.randint(0, V, (T, 2 * K), generator=g, device=DEV)
+    for call, targets in ((train.linear_cross_entropy, (batch[:, 1],)),
+                          (train.linear_distillation, (u.t(), ids[:, ::2]))):
+        grads = []
+        for ts in (targets, [t.contiguous() for t in targets]):
+            x, w = X.clone().requires_grad_(), W.clone().requires_grad_()
+            loss = call(x, w, *ts)
+            loss.sum().backward()
+            grads.append((loss, x.grad, w.grad))
+        assert equal(*grads)
+
+
+@pytest.mark.parametrize("lead", [(), (3,), (2, 5), (2, 0), (2, 3, 4)])
+def test_head_of_a_leading_shape(train, lead):
+    """The head takes [..., d], as the norm does, and gives a loss of that leading shape."""
+    d, V, K = 64, 300, 4
+    g = gen(5)
+    X = torch.randn((*lead, d), generator=g, device=DEV).to(torch.bfloat16)
+    W = torch.randn((V, d), generator=g, device=DEV).to(torch.bfloat16)
+    lab, ids = (torch.randint(0, V, s, generator=g, device=DEV) for s in (lead, (*lead, K)))
+    u = torch.randn((*lead, K), generator=g, device=DEV)
+    T = lab.numel()
+    for call, targets in ((train.linear_cross_entropy, (lab,)), (train.linear_distillation, (u, ids))):
+        x, x2 = X.clone().requires_grad_(), X.reshape(T, d).clone().requires_grad_()
+        loss = call(x, W, *targets)
+        flat = call(x2, W, *[t.reshape(T, *t.shape[len(lead):]) for t in targets])
+        assert loss.shape == lead and torch.equal(loss.reshape(T), flat)
+        loss.sum().backward()
+        flat.sum().backward()
+        assert torch.equal(x.grad.reshape(T, d), x2.grad)
+    x = torch.zeros((2, 3, d), dtype=torch.bfloat16, device=DEV)
+    for call in (lambda: train.linear_cross_entropy(x, W, torch.zeros(6, dtype=torch.int64, device=DEV)),
+                 lambda: train.linear_distillation(x, W, torch.zeros((2, 4, K), device=DEV),
+                                                   torch.zeros((2, 4, K), dtype=torch.int64, device=DEV))):
+        with pytest.raises(ValueError):
+            call()
