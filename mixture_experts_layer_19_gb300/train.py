@@ -18,6 +18,11 @@ contiguous CUDA tensors, 16-byte aligned; ValueError says what is wrong with
 an argument before anything is enqueued.  The differentiable functions and the
 modules first copy activations, targets, gradients and norm weights laid out
 otherwise.
+
+With `stream=` a call runs there and its outputs belong to that stream.  The
+caller makes it wait for what produces the inputs, and waits for it before
+using the outputs (which are dropped as torch has it: after record_stream where
+another stream reads them).  Inputs may be dropped right after the call.
 """
 from __future__ import annotations
 
@@ -70,10 +75,16 @@ def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     return t.clone() if t.data_ptr() % 16 else t
 
 
-def _elsewhere(index: int, stream: Optional[torch.cuda.Stream]):
+def _elsewhere(index: int, stream: Optional[torch.cuda.Stream], *inputs: Optional[torch.Tensor]):
     """The context a call has to run in when that is not the current one: the given stream, or the
-    tensors' GPU.  Outputs and workspace are then allocated there too."""
+    tensors' GPU.  Outputs and workspace are then allocated there too, and the memory of the inputs is not
+    handed out again, should the caller drop them, before the given stream is done with them."""
     if stream is not None:
+        if stream.device_index != index:
+            raise ValueError(f"stream: on cuda:{stream.device_index}, the tensors are on cuda:{index}")
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
         return torch.cuda.stream(stream)
     if index != torch.cuda.current_device():
         return torch.cuda.device(index)
@@ -148,7 +159,7 @@ def layer_norm_forward(x, weight, bias=None, eps: float = 1e-5, stream=None
         if bias.dtype is not weight.dtype or bias.shape != (d,):
             raise ValueError(f"bias: expected {weight.dtype} of shape {(d,)}, got {bias.dtype} of {tuple(bias.shape)}")
         bp = _ptr(bias, "bias", index)
-    there = _elsewhere(index, stream)
+    there = _elsewhere(index, stream, x, weight, bias)
     if there is not None:
         with there:
             return layer_norm_forward(x, weight, bias, eps)
@@ -180,7 +191,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, need_dx: bool = True, need_dw
     index = _device_of(x, "x")
     args = (_ptr(dy, "dy", index), _ptr(x, "x", index), _ptr(weight, "weight", index), _ptr(mean, "mean", index, 4),
             _ptr(rstd, "rstd", index, 4))
-    there = _elsewhere(index, stream)
+    there = _elsewhere(index, stream, dy, x, weight, mean, rstd)
     if there is not None:
         with there:
             return layer_norm_backward(dy, x, weight, mean, rstd, need_dx, need_dweight, need_dbias)
@@ -286,7 +297,7 @@ def cross_entropy_forward(X, W, labels, stream=None, wait_timeout_ns: int = 0, d
     _label_args(labels, T)
     index = _device_of(X, "X")
     args = (_ptr(X, "X", index), _ptr(W, "W", index), _ptr(labels, "labels", index, _ids_align(labels)))
-    there = _elsewhere(index, stream)
+    there = _elsewhere(index, stream, X, W, labels)
     if there is not None:
         with there:
             return cross_entropy_forward(X, W, labels, None, wait_timeout_ns, debug_flags)
@@ -316,7 +327,7 @@ def cross_entropy_backward(dloss, X, W, labels, lse, need_dX: bool = True, need_
     index = _device_of(X, "X")
     args = (_ptr(dloss, "dloss", index, 4), _ptr(X, "X", index), _ptr(W, "W", index),
             _ptr(labels, "labels", index, _ids_align(labels)), _ptr(lse, "lse", index, 4))
-    there = _elsewhere(index, stream)
+    there = _elsewhere(index, stream, dloss, X, W, labels, lse)
     if there is not None:
         with there:
             return cross_entropy_backward(dloss, X, W, labels, lse, need_dX, need_dW, piece, None, wait_timeout_ns,
@@ -349,7 +360,7 @@ def distill_forward(X, W, teacher_logits, teacher_ids, temperature: float = 1.0,
     args = (_ptr(X, "X", index), _ptr(W, "W", index),
             _ptr(teacher_logits, "teacher_logits", index, teacher_logits.element_size()),
             _ptr(teacher_ids, "teacher_ids", index, _ids_align(teacher_ids)))
-    there = _elsewhere(index, stream)
+    there = _elsewhere(index, stream, X, W, teacher_logits, teacher_ids)
     if there is not None:
         with there:
             return distill_forward(X, W, teacher_logits, teacher_ids, temperature, None, wait_timeout_ns, debug_flags)
@@ -369,7 +380,7 @@ def distill_backward(dloss, X, W, teacher_logits, teacher_ids, lse, temperature:
     args = (_ptr(dloss, "dloss", index, 4), _ptr(X, "X", index), _ptr(W, "W", index),
             _ptr(teacher_logits, "teacher_logits", index, teacher_logits.element_size()),
             _ptr(teacher_ids, "teacher_ids", index, _ids_align(teacher_ids)), _ptr(lse, "lse", index, 4))
-    there = _elsewhere(index, stream)
+    there = _elsewhere(index, stream, dloss, X, W, teacher_logits, teacher_ids, lse)
     if there is not None:
         with there:
             return distill_backward(dloss, X, W, teacher_logits, teacher_ids, lse, temperature, need_dX, need_dW, piece,
