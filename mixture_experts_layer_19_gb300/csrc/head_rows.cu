@@ -19,7 +19,9 @@ __device__ __forceinline__ int64_t load_id(const void* p, bool is64, int64_t i) 
 // One block per token.  Entry k is in use when its id lies in [0, V) and its
 // teacher logit is not -inf.  p = softmax of the logits in use over the
 // temperature; entries in use are stored by ascending id (ties by k), so that
-// a tile finds its own by binary search and equal ids keep one order.
+// a tile finds its own by binary search and equal ids keep one order.  What is
+// scaled is a logit's distance to the largest one, which no temperature turns
+// into infinity minus infinity: a mask of fp32's lowest value stays a finite logit.
 __global__ void __launch_bounds__(256) head_entries_kernel(const void* teacher, int teacher_bf16, const void* ids,
                                                            int ids64, int K, int Kp2, int64_t V, float inv_temp,
                                                            HeadRows r) {
@@ -37,9 +39,8 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const void* teacher, 
     unsigned long long kk = ~0ull;
     if (k < K) {
       const int64_t id = load_id(ids, ids64, t * K + k);
-      float v = teacher_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(teacher)[t * K + k])
-                             : reinterpret_cast<const float*>(teacher)[t * K + k];
-      v *= inv_temp;
+      const float v = teacher_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(teacher)[t * K + k])
+                                   : reinterpret_cast<const float*>(teacher)[t * K + k];
       const bool use = id >= 0 && id < V && v != -CUDART_INF_F;
       u[k] = use ? v : -CUDART_INF_F;
       if (use) {
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const void* teacher, 
   int c = 0;
   for (int k = tid; k < K; k += nt)
     if (key[k] != ~0ull) {
-      s += expf(u[(unsigned)key[k] & 2047u] - m);
+      s += expf((u[(unsigned)key[k] & 2047u] - m) * inv_temp);
       ++c;
     }
   for (int o = 16; o; o >>= 1) {
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(256) head_entries_kernel(const void* teacher, 
   for (int k = tid; k < K; k += nt) {
     const unsigned long long kk = key[k];
     if (kk == ~0ull) continue;
-    const float x = u[(unsigned)kk & 2047u] - m;
+    const float x = (u[(unsigned)kk & 2047u] - m) * inv_temp;
     const float p = expf(x) / s;
     r.ids[t * K + k] = (int32_t)(kk >> 11);
     r.probs[t * K + k] = p;
