@@ -428,6 +428,13 @@ typedef struct {
 moe_status_t moe_head_workspace_bytes(const moe_head_config_t* cfg, int32_t distill, int32_t backward,
                                       size_t* bytes);
 
+/* How a call is laid out on the device that is current, host-only: plan[6] =
+ * {CTAs that share a tile of the logits product, of dX, of dW (1 or 2); columns
+ * of a logits tile; parts that dX's sum over the vocabulary is split into;
+ * pieces of the vocabulary}.  What belongs to the backward is 0 with
+ * backward = 0, all of it with T = 0. */
+moe_status_t moe_head_info(const moe_head_config_t* cfg, int32_t distill, int32_t backward, int32_t* plan);
+
 /* Softmax cross entropy of each token's label:
  *   lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t[label_t]
  * A label outside [0, V) marks a token without a loss: loss_t = lse_t = 0,

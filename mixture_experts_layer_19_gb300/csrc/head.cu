@@ -409,6 +409,31 @@ moe_status_t moe_head_workspace_bytes(const moe_head_config_t* cfg, int32_t dist
   }
 }
 
+moe_status_t moe_head_info(const moe_head_config_t* cfg, int32_t distill, int32_t backward, int32_t* plan) {
+  const char* w = "moe_head_info";
+  try {
+    if (!plan) return bad(w, "null argument");
+    moe_status_t s = check_config(w, cfg, distill != 0);
+    if (s != MOE_OK) return s;
+    std::fill(plan, plan + 6, 0);
+    if (cfg->T == 0) return MOE_OK;
+    DeviceFacts f;
+    if ((s = device_facts(w, &f)) != MOE_OK) return s;
+    const Layout L = layout(*cfg, distill != 0, backward != 0, f.sms, f.pairs);
+    plan[0] = L.pair_z ? 2 : 1;
+    plan[3] = L.bn;
+    if (backward) {
+      plan[1] = L.pair_x ? 2 : 1;
+      plan[2] = L.pair_w ? 2 : 1;
+      plan[4] = L.nsplit;
+      plan[5] = (int32_t)ceil_div(cfg->V, L.piece);
+    }
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
 moe_status_t moe_cross_entropy_forward(const moe_head_config_t* cfg, const void* X, const void* W, const void* labels,
                                        float* loss, float* lse, void* workspace, size_t workspace_bytes,
                                        int32_t* status, moe_stream_t stream) {

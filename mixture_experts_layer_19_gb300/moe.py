@@ -41,7 +41,7 @@ EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_saved_bytes", "moe_forward", "m
             "moe_plan_info", "moe_nv_tensor_scale", "moe_nv_quantize", "moe_nv_quantize_transposed",
             "moe_nv_weight_scales", "moe_debug_quant_dump", "moe_plan_padded_rows",
             "moe_layer_norm_forward", "moe_layer_norm_workspace_bytes", "moe_layer_norm_backward",
-            "moe_head_workspace_bytes", "moe_cross_entropy_forward", "moe_cross_entropy_backward",
+            "moe_head_workspace_bytes", "moe_head_info", "moe_cross_entropy_forward", "moe_cross_entropy_backward",
             "moe_distill_forward", "moe_distill_backward")
 
 
@@ -95,6 +95,7 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         "moe_layer_norm_workspace_bytes": [I64, I64, ctypes.POINTER(ctypes.c_size_t)],
         "moe_layer_norm_backward": [VP, VP, VP, FP, FP, I64, I64, I32, I32, VP, VP, VP, VP, ctypes.c_size_t, P],
         "moe_head_workspace_bytes": [HC, I32, I32, ctypes.POINTER(ctypes.c_size_t)],
+        "moe_head_info": [HC, I32, I32, ctypes.POINTER(I32)],
         "moe_cross_entropy_forward": [HC, VP, VP, VP, FP, FP, VP, ctypes.c_size_t, VP, P],
         "moe_cross_entropy_backward": [HC, FP, VP, VP, VP, FP, VP, VP, VP, ctypes.c_size_t, VP, P],
         "moe_distill_forward": [HC, VP, VP, VP, VP, FP, FP, VP, ctypes.c_size_t, VP, P],

@@ -284,6 +284,14 @@ def _head_workspace_bytes(T, V, d, K, piece, backward, index) -> int:
     return n.value
 
 
+def head_info(T: int, V: int, d: int, K: int = 0, backward: bool = False, piece: int = 0) -> dict:
+    """How a call of these sizes is laid out on the current GPU (K = 0: cross entropy), as moe_head_info states it."""
+    cfg = moe_head_config_t(T, V, d, K, 1.0, 0, 0, piece, 0, 0)
+    plan = (ctypes.c_int32 * 6)()
+    _check(moe.lib().moe_head_info(ctypes.byref(cfg), K > 0, backward, plan), "moe_head_info")
+    return dict(zip(("logits_ctas", "dX_ctas", "dW_ctas", "logits_columns", "dX_splits", "pieces"), plan))
+
+
 def _ids_align(t) -> int:
     return 8 if t.dtype is _I64 else 4
 
