@@ -1,0 +1,53 @@
+"""GPU tests of layer norm's sums over many rows, and of long rows in number.
+
+Tolerance of the column sums.  A block adds up its rows one by one, at least one block per SM (or
+32 slices of the rows past 8192 elements); then 32 slices of at most 8 * SMs / 32 blocks are added one by
+one, then the slices: each addition is off by u32 of the magnitudes so far, and a term by 4 u32.  That is
+far less than any one row adds, so a row left out or added twice shows."""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_19_gb300.workload import to_f64
+from oracle import train_ref
+from tests.test_gpu_train import check_ln, ln_inputs, within
+
+pytestmark = pytest.mark.gpu
+U16, U32 = 2.0 ** -8, 2.0 ** -24
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def train():
+    from mixture_experts_layer_19_gb300 import train
+    yield train
+    assert train.device_status(0) == 0
+
+
+@pytest.mark.parametrize("rows,d,xt", [(10007, 64, BF), (10007, 64, F32), (3001, 257, BF), (5000, 1001, F32),
+                                       (2049, 1024, BF), (4096, 2048, BF), (1000, 7168, F32), (700, 9001, BF),
+                                       (700, 9001, F32), (2000, 8200, BF), (2000, 8200, F32), (33, 8200, BF)])
+def test_column_sums(train, rows, d, xt):
+    x, w, _, dy = ln_inputs(rows, d, xt, F32, seed=rows + d)
+    X, DY = to_f64(x), to_f64(dy)
+    _, mean, rstd = train.layer_norm_forward(x.to(DEV), w.to(DEV))
+    _, dw, db = train.layer_norm_backward(dy.to(DEV), x.to(DEV), w.to(DEV), mean, rstd)
+    sm, sr = to_f64(mean), to_f64(rstd)
+    _, rw, rb = train_ref.layer_norm_backward(DY, X, to_f64(w), sm, sr)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    blocks = min(rows, sms if d <= 8192 else 32)
+    chain = (-(-rows // blocks) + -(-8 * sms // 32) + 32) * U32
+    n = np.abs(X - sm[:, None]) * sr[:, None]
+    off = (chain + 4 * U32) * (np.abs(DY) * n).sum(0), chain * np.abs(DY).sum(0)
+    # a row's own share of db is over the bound in all but a few columns
+    assert (np.median(np.abs(DY), axis=0) > 2 * off[1]).mean() > 0.9
+    within(dw, rw, off[0] + U32 * np.abs(rw))
+    within(db, rb, off[1] + U32 * np.abs(rb))
+
+
+@pytest.mark.parametrize("rows,d,xt", [(700, 9001, BF), (700, 9001, F32), (2000, 8200, BF), (2000, 8200, F32),
+                                       (2000, 12288, BF), (700, 16384, BF), (700, 12288, F32)])
+def test_long_rows_in_number(train, rows, d, xt):
+    """More rows than blocks, where rows are read again, and bf16 rows of up to 16384 that four warps hold."""
+    check_ln(train, *ln_inputs(rows, d, xt, F32, seed=rows))
