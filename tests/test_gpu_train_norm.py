@@ -26,7 +26,7 @@ def train():
 
 
 @pytest.mark.parametrize("rows,d,xt", [(10007, 64, BF), (10007, 64, F32), (3001, 257, BF), (5000, 1001, F32),
-                                       (2049, 1024, BF), (4096, 2048, BF), (1000, 7168, F32), (700, 9001, BF),
+                                       (2500, 691, F32), (2049, 1024, BF), (4096, 2048, BF), (1000, 7168, F32), (700, 9001, BF),
                                        (700, 9001, F32), (2000, 8200, BF), (2000, 8200, F32), (33, 8200, BF)])
 def test_column_sums(train, rows, d, xt):
     x, w, _, dy = ln_inputs(rows, d, xt, F32, seed=rows + d)
