@@ -91,6 +91,24 @@ __device__ __forceinline__ void block_sum(float (&s)[NV], float (*red)[NV], int 
     for (int i = 0; i < NV; ++i) s[i] += red[w][i];
 }
 
+// The mean of a row is off by a few units of its last place, which is far from nothing beside a small spread:
+// rows of a constant 12345 came out as 0.3.  bf16 rows far from zero hold multiples of one unit, and their
+// sum is exact up to 2^16 elements: mean_of, s times 1 / d corrected once by what it leaves of s, gives
+// their mean to the last place.  An fp32 row whose mean is more than 16 spreads from zero is done over: the
+// mean of the deviations corrects the mean, and the variance about it.  (Adding the deviations up beside
+// the squares of every row cost 91 us instead of 82 at 16384 x 7168, bf16, and 36 instead of 29 at 131072 x 256;
+// a division in place of the correction, 33.)
+__device__ __forceinline__ float mean_of(float s, float d, float inv_d) {
+  const float m = s * inv_d, c = fmaf(fmaf(-m, d, s), inv_d, m);
+  return c == c ? c : m;                 // an infinite sum leaves no remainder
+}
+__device__ __forceinline__ bool mean_far(float m, float rs) { return fabsf(m * rs) > 16.0f; }
+__device__ __forceinline__ void correct_mean(float dev, float& m, float& var) {
+  m += dev;
+  var = fmaf(-dev, dev, var);
+  if (var < 0.0f) var = 0.0f;            // a NaN stays
+}
+
 template <class XT, class WT, int VW, int VPT>
 __global__ void __launch_bounds__(kMaxThreads) ln_fwd_kernel(const XT* __restrict__ x, const WT* __restrict__ w,
                                                              const WT* __restrict__ b, int64_t rows, int d, float eps,
@@ -99,7 +117,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_kernel(const XT* __restric
   pdl_wait();
   pdl_release();
   using V = Vec<XT, VW>;
-  __shared__ float red[2][16][1];
+  __shared__ float red[3][16][1];
   const int vecs = d / VW, nw = blockDim.x >> 5, tid = threadIdx.x;
   const float inv_d = 1.0f / (float)d;
   float wr[VPT][VW], br[VPT][VW];
@@ -138,7 +156,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_kernel(const XT* __restric
     }
     if (r + gridDim.x < rows) fetch(r + gridDim.x);
     block_sum<1>(s, red[0], nw);
-    const float m = s[0] * inv_d;
+    float m = mean_of(s[0], (float)d, inv_d);
     float q[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -150,7 +168,21 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_kernel(const XT* __restric
       }
     }
     block_sum<1>(q, red[1], nw);
-    const float rs = 1.0f / sqrtf(q[0] * inv_d + eps);
+    float var = q[0] * inv_d, off = 0.0f;
+    float rs = 1.0f / sqrtf(var + eps);
+    if (mean_far(m, rs)) {
+      q[0] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (tid + j * blockDim.x < vecs)
+#pragma unroll
+          for (int i = 0; i < VW; ++i) q[0] += v[j][i];
+      block_sum<1>(q, red[2], nw);
+      off = m;
+      correct_mean(q[0] * inv_d, m, var);
+      off = m - off;
+      rs = 1.0f / sqrtf(var + eps);
+    }
     V* dst = reinterpret_cast<V*>(y + r * d);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -158,7 +190,7 @@ __global__ void __launch_bounds__(kMaxThreads) ln_fwd_kernel(const XT* __restric
       if (c < vecs) {
         V o;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) o.v[i] = from_f<XT>(fmaf(v[j][i] * rs, wr[j][i], br[j][i]));
+        for (int i = 0; i < VW; ++i) o.v[i] = from_f<XT>(fmaf((v[j][i] - off) * rs, wr[j][i], br[j][i]));
         dst[c] = o;
       }
     }
@@ -263,7 +295,7 @@ __global__ void __launch_bounds__(row_warps(NV) * 32, 1) ln_fwd_rows_kernel(cons
   using P = Pairs<XT>;
   constexpr int kRowWarps = row_warps(NV);
   extern __shared__ float4 wb[];                         // [P::n][vecs]
-  __shared__ float red[2][kRowWarps];
+  __shared__ float red[4][kRowWarps];
   const int vecs = d / (2 * P::n);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < vecs * P::n; i += kRowWarps * 32) {
@@ -287,6 +319,43 @@ __global__ void __launch_bounds__(row_warps(NV) * 32, 1) ln_fwd_rows_kernel(cons
     }
     return s;
   };
+  // An fp32 row far from zero, from its first mean on.  Rare, so it is read again: keeping it in registers
+  // for this would cost every row.
+  [[maybe_unused]] auto redo = [&](int64_t r, float m) {
+    const uint4* src = x + r * vecs;
+    f2 s2 = f2_make(0, 0), c2 = s2;
+    const f2 mm = f2_make(-m, -m);
+#pragma unroll 1
+    for (int c = tid; c < vecs; c += nt) {
+      const uint4 u = src[c];
+#pragma unroll
+      for (int p = 0; p < P::n; ++p) {
+        const f2 a = f2_add(P::get(u, p), mm);
+        s2 = f2_fma(a, a, s2);
+        c2 = f2_add(c2, a);
+      }
+    }
+    const float2 s = f2_get(s2), t = f2_get(c2);
+    float var = row_sum(s.x + s.y, red[2]) * inv_d;
+    correct_mean(row_sum(t.x + t.y, red[3]) * inv_d, m, var);
+    const float rs = 1.0f / sqrtf(var + eps);
+#pragma unroll 1
+    for (int c = tid; c < vecs; c += nt) {
+      const uint4 u = src[c];
+      uint4 o;
+#pragma unroll
+      for (int p = 0; p < P::n; ++p) {
+        const float4 q = wb[p * vecs + c];
+        P::set(o, p, f2_fma(f2_mul(f2_add(P::get(u, p), f2_make(-m, -m)), f2_make(rs, rs)), f2_make(q.x, q.y),
+                            f2_make(q.z, q.w)));
+      }
+      __stcs(y + r * vecs + c, o);
+    }
+    if (tid == 0) {
+      mean[r] = m;
+      rstd[r] = rs;
+    }
+  };
   for (int64_t r = (int64_t)blockIdx.x * groups + group; r < rows; r += (int64_t)gridDim.x * groups) {
     const uint4* src = x + r * vecs;
     uint4 v[NV];
@@ -305,7 +374,7 @@ __global__ void __launch_bounds__(row_warps(NV) * 32, 1) ln_fwd_rows_kernel(cons
       }
     keep_packed<NV>(v);
     float2 s = f2_get(f2_add(s2, t2));
-    const float m = row_sum(s.x + s.y, red[0]) * inv_d;
+    const float m = mean_of(row_sum(s.x + s.y, red[0]), (float)d, inv_d);
     const f2 mm = f2_make(-m, -m);
     s2 = t2 = f2_make(0, 0);
 #pragma unroll
@@ -322,22 +391,26 @@ __global__ void __launch_bounds__(row_warps(NV) * 32, 1) ln_fwd_rows_kernel(cons
     s = f2_get(f2_add(s2, t2));
     const float rs = 1.0f / sqrtf(row_sum(s.x + s.y, red[1]) * inv_d + eps);
     const f2 rr = f2_make(rs, rs);
+    if (sizeof(XT) == 4 && mean_far(m, rs)) {
+      redo(r, m);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = tid + j * nt;
-      if (c < vecs) {
-        uint4 o;
+      for (int j = 0; j < NV; ++j) {
+        const int c = tid + j * nt;
+        if (c < vecs) {
+          uint4 o;
 #pragma unroll
-        for (int p = 0; p < P::n; ++p) {
-          const float4 q = wb[p * vecs + c];
-          P::set(o, p, f2_fma(f2_mul(f2_add(P::get(v[j], p), mm), rr), f2_make(q.x, q.y), f2_make(q.z, q.w)));
+          for (int p = 0; p < P::n; ++p) {
+            const float4 q = wb[p * vecs + c];
+            P::set(o, p, f2_fma(f2_mul(f2_add(P::get(v[j], p), mm), rr), f2_make(q.x, q.y), f2_make(q.z, q.w)));
+          }
+          __stcs(y + r * vecs + c, o);
         }
-        __stcs(y + r * vecs + c, o);
       }
-    }
-    if (tid == 0) {
-      mean[r] = m;
-      rstd[r] = rs;
+      if (tid == 0) {
+        mean[r] = m;
+        rstd[r] = rs;
+      }
     }
   }
 }
@@ -389,7 +462,7 @@ __global__ void __launch_bounds__(512, 2) ln_fwd_narrow_kernel(const uint4* __re
       for (int u = 0; u < kNarrowSets; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
 #pragma unroll
     for (int u = 0; u < kNarrowSets; ++u) {
-      m[u] = s[u] * inv_d;
+      m[u] = mean_of(s[u], (float)d, inv_d);
       const f2 mm = f2_make(-m[u], -m[u]);
       f2 t = f2_make(0, 0);
 #pragma unroll
@@ -403,19 +476,62 @@ __global__ void __launch_bounds__(512, 2) ln_fwd_narrow_kernel(const uint4* __re
     for (int o = G >> 1; o; o >>= 1)
 #pragma unroll
       for (int u = 0; u < kNarrowSets; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+    bool any = false;
 #pragma unroll
     for (int u = 0; u < kNarrowSets; ++u) {
       const int64_t r = r0 + u * per;
       const float rs = 1.0f / sqrtf(s[u] * inv_d + eps);
+      const bool far = sizeof(XT) == 4 && mean_far(m[u], rs);
+      any |= far;
       const f2 rr = f2_make(rs, rs), mm = f2_make(-m[u], -m[u]);
-      if (in && r < rows) {
+      if (in && r < rows && !far) {
         uint4 o;
 #pragma unroll
         for (int p = 0; p < P::n; ++p) P::set(o, p, f2_fma(f2_mul(f2_add(P::get(v[u], p), mm), rr), wr[p], br[p]));
         __stcs(y + r * vecs + c, o);
       }
-      if (c == 0 && r < rows) {
+      if (c == 0 && r < rows && !far) {
         mean[r] = m[u];
+        rstd[r] = rs;
+      }
+    }
+    if (!__any_sync(0xffffffffu, any)) continue;
+    // rare, so the rows are read again, one set at a time; the sums of the same values come out the same
+#pragma unroll 1
+    for (int u = 0; u < kNarrowSets; ++u) {
+      const int64_t r = r0 + u * per;
+      const uint4 q = in && r < rows ? __ldcs(x + r * vecs + c) : make_uint4(0, 0, 0, 0);
+      auto sum = [&](f2 t) {
+        const float2 f = f2_get(t);
+        float a = in ? f.x + f.y : 0.0f;
+        for (int o = G >> 1; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        return a;
+      };
+      f2 t = P::get(q, 0);
+#pragma unroll
+      for (int p = 1; p < P::n; ++p) t = f2_add(t, P::get(q, p));
+      float mu = mean_of(sum(t), (float)d, inv_d);
+      f2 sq = f2_make(0, 0), dev = sq;
+#pragma unroll
+      for (int p = 0; p < P::n; ++p) {
+        const f2 a = f2_add(P::get(q, p), f2_make(-mu, -mu));
+        sq = f2_fma(a, a, sq);
+        dev = f2_add(dev, a);
+      }
+      float var = sum(sq) * inv_d;
+      const bool far = mean_far(mu, 1.0f / sqrtf(var + eps));
+      correct_mean(sum(dev) * inv_d, mu, var);
+      if (!far || r >= rows) continue;
+      const float rs = 1.0f / sqrtf(var + eps);
+      if (in) {
+        uint4 o;
+#pragma unroll
+        for (int p = 0; p < P::n; ++p)
+          P::set(o, p, f2_fma(f2_mul(f2_add(P::get(q, p), f2_make(-mu, -mu)), f2_make(rs, rs)), wr[p], br[p]));
+        __stcs(y + r * vecs + c, o);
+      }
+      if (c == 0) {
+        mean[r] = mu;
         rstd[r] = rs;
       }
     }
@@ -627,7 +743,7 @@ __global__ void __launch_bounds__(kOddWarps * 32, 1) ln_fwd_odd_kernel(const XT*
   pdl_wait();
   pdl_release();
   extern __shared__ float2 wb2[];                        // [d]
-  __shared__ float red[2][kOddWarps];
+  __shared__ float red[3][kOddWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < d; i += kOddWarps * 32)
     wb2[i] = make_float2(weight_at(w, w_f32, i), b ? weight_at(b, w_f32, i) : 0.0f);
@@ -653,21 +769,40 @@ __global__ void __launch_bounds__(kOddWarps * 32, 1) ln_fwd_odd_kernel(const XT*
     for (int j = 0; j < kOddElems; ++j) v[j] = tid + j * nt < d ? to_f(src[tid + j * nt]) : 0.0f;
 #pragma unroll
     for (int j = 0; j < kOddElems; ++j) s += v[j];
-    const float m = row_sum(s, red[0]) * inv_d;
+    float m = mean_of(row_sum(s, red[0]), (float)d, inv_d);
     s = 0.0f;
 #pragma unroll
     for (int j = 0; j < kOddElems; ++j) {
       v[j] -= m;
       if (tid + j * nt < d) s = fmaf(v[j], v[j], s);
     }
-    const float rs = 1.0f / sqrtf(row_sum(s, red[1]) * inv_d + eps);
+    float var = row_sum(s, red[1]) * inv_d;
+    float rs = 1.0f / sqrtf(var + eps);
+    if (sizeof(XT) == 2 || !mean_far(m, rs)) {
 #pragma unroll
-    for (int j = 0; j < kOddElems; ++j) {
-      const int c = tid + j * nt;
-      if (c < d) {
-        const float2 q = wb2[c];
-        y[r * d + c] = from_f<XT>(fmaf(v[j] * rs, q.x, q.y));
+      for (int j = 0; j < kOddElems; ++j) {
+        const int c = tid + j * nt;
+        if (c < d) {
+          const float2 q = wb2[c];
+          y[r * d + c] = from_f<XT>(fmaf(v[j] * rs, q.x, q.y));
+        }
       }
+      if (tid == 0) {
+        mean[r] = m;
+        rstd[r] = rs;
+      }
+      continue;
+    }
+    // rare, so the row is read again
+    s = 0.0f;
+#pragma unroll 1
+    for (int c = tid; c < d; c += nt) s += to_f(src[c]) - m;
+    correct_mean(row_sum(s, red[2]) * inv_d, m, var);
+    rs = 1.0f / sqrtf(var + eps);
+#pragma unroll 1
+    for (int c = tid; c < d; c += nt) {
+      const float2 q = wb2[c];
+      y[r * d + c] = from_f<XT>(fmaf((to_f(src[c]) - m) * rs, q.x, q.y));
     }
     if (tid == 0) {
       mean[r] = m;
@@ -794,19 +929,27 @@ __global__ void __launch_bounds__(512) ln_fwd_long_kernel(const XT* __restrict__
                                                           float* __restrict__ rstd) {
   pdl_wait();
   pdl_release();
-  __shared__ float red[2][16][1];
+  __shared__ float red[3][16][1];
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const XT* src = x + r * d;
     float s[1] = {0.0f}, q[1] = {0.0f};
     for (int64_t c = threadIdx.x; c < d; c += 512) s[0] += to_f(src[c]);
     block_sum<1>(s, red[0], 16);
-    const float m = s[0] / (float)d;
+    float m = s[0] / (float)d;
     for (int64_t c = threadIdx.x; c < d; c += 512) {
       const float v = to_f(src[c]) - m;
       q[0] = fmaf(v, v, q[0]);
     }
     block_sum<1>(q, red[1], 16);
-    const float rs = 1.0f / sqrtf(q[0] / (float)d + eps);
+    float var = q[0] / (float)d;
+    float rs = 1.0f / sqrtf(var + eps);
+    if (mean_far(m, rs)) {
+      s[0] = 0.0f;
+      for (int64_t c = threadIdx.x; c < d; c += 512) s[0] += to_f(src[c]) - m;
+      block_sum<1>(s, red[2], 16);
+      correct_mean(s[0] / (float)d, m, var);
+      rs = 1.0f / sqrtf(var + eps);
+    }
     for (int64_t c = threadIdx.x; c < d; c += 512)
       y[r * d + c] = from_f<XT>(fmaf((to_f(src[c]) - m) * rs, to_f(w[c]), b ? to_f(b[c]) : 0.0f));
     if (threadIdx.x == 0) {

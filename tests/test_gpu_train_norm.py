@@ -51,3 +51,37 @@ def test_column_sums(train, rows, d, xt):
 def test_long_rows_in_number(train, rows, d, xt):
     """More rows than blocks, where rows are read again, and bf16 rows of up to 16384 that four warps hold."""
     check_ln(train, *ln_inputs(rows, d, xt, F32, seed=rows))
+
+
+@pytest.mark.parametrize("rows,d", [(3, 64), (3, 691), (3, 1001), (3, 7168), (3, 8200), (3, 9001), (2000, 64),
+                                    (2000, 256), (2000, 691), (2000, 2051), (2000, 7168), (700, 9001)])
+@pytest.mark.parametrize("xt", [BF, F32])
+@pytest.mark.parametrize("value", [3.3, 1000.0, 12345.6, 1e6])
+def test_rows_of_one_value(train, rows, d, xt, value):
+    """The mean of such a row is its value, and nothing is left of it.  The first mean is off by at most 512 u32
+    of the value (its sum's chain); the mean of the deviations, all the same, restores it to the bit, since
+    that is off by 512 u32 of 512 units of the last place, less than half of one."""
+    x = torch.full((rows, d), value, device=DEV).to(xt)
+    w, b = torch.full((d,), 1.5, device=DEV), torch.full((d,), 0.25, device=DEV)
+    y, mean, rstd = train.layer_norm_forward(x, w, b)
+    assert (mean == x[0, 0].float()).all() and (y == 0.25).all()
+    # the deviations' squares cancel to 512 u32 of (512 u32 value)^2
+    off = 512 * U32 * (512 * U32 * value) ** 2 + 4 * U32 * 1e-5
+    assert ((rstd.double() ** -2 - 1e-5).abs() <= off + 4 * U32 * 1e-5).all()
+
+
+@pytest.mark.parametrize("rows,d", [(7, 64), (7, 1001), (7, 7168), (7, 9001), (2000, 256), (2000, 1001), (2000, 7168)])
+def test_mean_far_from_zero(train, rows, d):
+    """The mean is right to its last place (u32 of it, and the deviations' own chain), so a row's values are off
+    by that much of the spread, and no more, however long the row."""
+    x, w, b, _ = ln_inputs(rows, d, F32, F32, seed=d, shift=5000.0)
+    X = to_f64(x)
+    ry, rm, rr = train_ref.layer_norm(X, to_f64(w), to_f64(b), 1e-5)
+    y, mean, rstd = train.layer_norm_forward(x.to(DEV), w.to(DEV), b.to(DEV))
+    e = 512 * U32
+    spread = np.abs(X - rm[:, None])
+    dm = 2 * U32 * np.abs(rm) + e * (spread.mean(1) + 512 * U32 * np.abs(rm))
+    within(mean, rm, dm)
+    n_off = (e * spread + dm[:, None]) * rr[:, None]
+    y_off = n_off * np.abs(to_f64(w)) + 8 * U32 * (np.abs(ry) + np.abs(to_f64(b)))
+    within(y, ry, y_off)
