@@ -424,7 +424,17 @@ typedef struct {
 } moe_head_config_t;
 
 /* Bytes of workspace one call needs (256-byte aligned; for the device that
- * is current). */
+ * is current).  Most of it, with T rounded up to 256:
+ *   both directions  a copy of X, 2 d bytes per token
+ *   forward          16 bytes per token and 256 columns of the vocabulary (64 to
+ *                    256 with up to 64 tokens)
+ *   backward         a piece of D, 2 bytes per token and column: with piece = 0
+ *                    256 MB, or 8192 columns (16 KB per token) where that is more,
+ *                    which is from 16384 tokens on; and, with several pieces
+ *                    or where dX's sum over the vocabulary is split, fp32 sums of dX,
+ *                    4 d bytes per token and split (moe_head_info)
+ *   distillation     8 K + V / 64 bytes per token, 4 K more forward
+ */
 moe_status_t moe_head_workspace_bytes(const moe_head_config_t* cfg, int32_t distill, int32_t backward,
                                       size_t* bytes);
 

@@ -23,7 +23,9 @@ using namespace moe;
 
 constexpr int kMaxDevices = 64;
 
-constexpr int64_t kPieceBytes = int64_t(256) << 20;   // default size of the D piece
+// Default piece of D: this much, but no fewer columns than keep its products wide (16 KB per token, the
+// larger of the two from 16384 tokens on).
+constexpr int64_t kPieceBytes = int64_t(256) << 20, kPieceColumns = 8192;
 
 moe_status_t bad(const char* where, const char* what, moe_status_t s = MOE_ERR_INVALID_ARG) {
   set_error_detail((std::string(where) + ": " + what).c_str());
@@ -137,7 +139,7 @@ Layout layout(const moe_head_config_t& c, bool distill, bool backward, int sms, 
   L.Tp = std::max<int64_t>(up(c.T, kHeadRowPad), kHeadRowPad);
   L.nsplit = 1;
   if (backward) {
-    int64_t p = c.piece > 0 ? up(c.piece, 256) : std::max<int64_t>(kPieceBytes / (2 * L.Tp), 8192);
+    int64_t p = c.piece > 0 ? up(c.piece, 256) : std::max(kPieceBytes / (2 * L.Tp), kPieceColumns);
     const int64_t n = std::max<int64_t>(1, ceil_div(up(c.V, 256), p));
     L.piece = up(ceil_div(c.V, n), 256);        // pieces of equal size
     L.ldl = L.piece;

@@ -327,8 +327,8 @@ def cross_entropy_backward(dloss, X, W, labels, lse, need_dX: bool = True, need_
                            stream=None, wait_timeout_ns: int = 0, debug_flags: int = 0):
     """(dX, dW) bf16 for the upstream gradient dloss fp32 [T] and the forward's lse; None for what is not needed.
 
-    `piece`: vocabulary columns handled at a time (0: a default that keeps
-    the piece's workspace near 256 MB)."""
+    `piece`: vocabulary columns handled at a time (0: as many as take 256 MB of
+    workspace, but no fewer than 8192, which take 16 KB per token)."""
     T, d, V = _head_args(X, W)
     _label_args(labels, T)
     _row_vectors(T, dloss, lse)

@@ -122,3 +122,18 @@ def test_expired_wait_of_a_pair(train):
     assert train.device_status(0) == 0
     assert same_bits((loss, lse), train.cross_entropy_forward(X, W, lab))
     assert same_bits(grads, train.cross_entropy_backward(dl, X, W, lab, lse))
+
+
+@pytest.mark.parametrize("T,d,V,K", [(40, 264, 20011, 0), (300, 1032, 1000, 7), (4096, 256, 40000, 0), (20000, 64, 9000, 5),
+                                     (131072, 512, 32768, 0), (1 << 20, 64, 100000, 0)])
+def test_workspace_is_what_the_header_says(train, T, d, V, K):
+    Tp = -(-T // 256) * 256
+    forward, backward = (train.head_info(T, V, d, K, b) for b in (False, True))
+    common = Tp * (2 * d + 64) + K * Tp * 8 + (Tp * V / 64 + Tp * 4 if K else 0) + 65536
+    part = 16 * Tp * (V // forward["logits_columns"] + 1) + 4 * Tp * max(K, 1)
+    assert train._head_workspace_bytes(T, V, d, K, 0, False, 0) <= common + part
+    piece = max(256 << 20, 16384 * Tp) + 512 * Tp                       # pieces are multiples of 256 columns
+    sums = 4 * d * Tp * backward["dX_splits"] if backward["dX_splits"] > 1 or backward["pieces"] > 1 else 0
+    got = train._head_workspace_bytes(T, V, d, K, 0, True, 0)
+    assert got <= common + min(piece, 2 * Tp * (V + 256)) + sums
+    assert got >= min(piece / 2, 2 * Tp * V) + sums                      # and not far below: pieces of equal size
