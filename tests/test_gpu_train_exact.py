@@ -104,3 +104,28 @@ def test_distillation_of_a_student_that_agrees(train, T, temp):
     Xd, Wd, td, idd, Gd = X.to(DEV), W.to(DEV), teacher.to(DEV), ids.to(DEV), G.to(DEV)
     check(train, X, W, P, on, ent, temp, lambda: train.distill_forward(Xd, Wd, td, idd, temp),
           lambda lse: train.distill_backward(Gd, Xd, Wd, td, idd, lse, temp), G)
+
+
+@pytest.mark.parametrize("T", [1, 16, 40, 100, 300])
+@pytest.mark.parametrize("d", [520, 1032, 7168])
+def test_vocabulary_of_one_has_no_gradient(train, T, d):
+    """D = exp(z - lse) - 1 with lse = z + log s, where s is 1 to within 2^-21: for z past 16 that is less than
+    half a unit of its last place, so lse is z, if the two directions' logits agree to the bit, and D is 0."""
+    g = gen(T + d)
+    X = (torch.rand((T, d), generator=g) + 0.1).to(torch.bfloat16).to(DEV)
+    W = ((torch.rand((1, d), generator=g) + 0.1) * (64 / d)).to(torch.bfloat16).to(DEV)
+    labels = torch.zeros(T, dtype=torch.int64, device=DEV)
+    loss, lse = train.cross_entropy_forward(X, W, labels)
+    dX, dW = train.cross_entropy_backward(torch.ones(T, device=DEV), X, W, labels, lse)
+    assert (lse > 16).all() and all((t == 0).all() for t in (loss, dX, dW))
+
+
+@pytest.mark.parametrize("T,d,V,piece", [(300, 7168, 20000, 1024), (300, 1032, 4000, 256), (40, 2056, 5000, 512)])
+def test_logits_do_not_depend_on_the_tiles(train, T, d, V, piece):
+    """dW of a piece is D^T X of its own columns: pieces, and with them CTA pairs and tile widths, change no bit."""
+    X, W, labels, g = confident_inputs(T, d, V, T, (0.0, 12.0))
+    Xd, Wd, lab, G = X.to(DEV), W.to(DEV), labels.to(DEV), torch.rand(T, generator=g).to(DEV)
+    _, lse = train.cross_entropy_forward(Xd, Wd, lab)
+    whole = train.cross_entropy_backward(G, Xd, Wd, lab, lse)
+    cut = train.cross_entropy_backward(G, Xd, Wd, lab, lse, piece=piece)
+    assert torch.equal(whole[1], cut[1])
