@@ -450,7 +450,8 @@ moe_status_t moe_head_info(const moe_head_config_t* cfg, int32_t distill, int32_
  * A label outside [0, V) marks a token without a loss: loss_t = lse_t = 0,
  * and whatever its row of X holds takes part in nothing.
  *   X [T, d] bf16, W [V, d] bf16, labels [T];  loss, lse [T] fp32, written.
- * Logits are bf16 products in fp32 sums (exact to about 1e-6 of a logit).
+ * Logits are bf16 products in fp32 sums (exact to about 1e-6 of a logit), the
+ * same to the bit in both directions and however the vocabulary is cut.
  * status: a device int32 that receives MOE_ERR_TIMEOUT when a device-side
  * wait expires (outputs are then not valid), or NULL; it is never cleared.
  * Errors, synchronous with nothing enqueued: MOE_ERR_INVALID_ARG for a null
@@ -480,8 +481,9 @@ moe_status_t moe_cross_entropy_backward(const moe_head_config_t* cfg, const floa
  *   lse_t = log sum_v exp(z_tv / s),
  *   loss_t = s^2 sum_k p_tk (log p_tk - log q_t[ids_tk])
  * (s^2 keeps the gradient's size as the temperature changes).  An entry whose
- * id lies outside [0, V), or whose logit is -inf, is not in use; equal ids
- * add up.  A token without entries has no loss (as above).
+ * id lies outside [0, V), or whose logit is -inf, is not in use (a finite mask,
+ * such as the type's lowest value, is a logit); equal ids add up.  A token
+ * without entries has no loss (as above).
  *   teacher [T, K] fp32 or bf16, ids [T, K]; the rest as above. */
 moe_status_t moe_distill_forward(const moe_head_config_t* cfg, const void* X, const void* W, const void* teacher,
                                  const void* ids, float* loss, float* lse, void* workspace,

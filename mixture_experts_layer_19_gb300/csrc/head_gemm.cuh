@@ -19,9 +19,9 @@
 // next tile's products.  Tiles are handed out statically and every sum has
 // one fixed order: bitwise repeatable.
 //
-// Measured at 2048 tokens, 7168 x 32768 (0.96 TFLOP each): D 514 us, dX 484,
-// dW 502, tensor pipe 88, 94 and 87% busy; back to back the power limit holds
-// them to 1.67 PFLOP/s, and 4096 tokens' forward at 7168 x 65536 to 1.61.  With
+// Measured at 2048 tokens, 7168 x 32768 (0.96 TFLOP each): D 546 us, dX 486,
+// dW 497, tensor pipe 80, 93 and 87% busy; back to back the power limit holds
+// them to 1.65 PFLOP/s, and 4096 tokens' forward at 7168 x 65536 to 1.62.  With
 // few tokens reading W bounds the forward (one token, 7168 x 400000: 6.9 TB/s).
 // Rows whose byte length is not a multiple of 32 cost the products a quarter
 // (width 1000 against 1008): each row of a TMA box then touches one sector more.
@@ -35,7 +35,7 @@
 // the log-sum-exp was taken of.  With D in one run over K, gradients of tokens
 // predicted with 0.997 to 0.9995 at width 7168, from logits of 40, were off by 40%
 // (norm of a row of dX); in parts they are off by 0.24%.  The sums dX and dW, of
-// entries of D that were rounded to bf16, do not need it.
+// entries of D that were rounded to bf16, do not need it.  (D in one run took 514 us.)
 #pragma once
 #include "head.h"
 #include "pdl.cuh"
@@ -63,8 +63,8 @@ constexpr int logits_chunk(int arows) { return arows == kHBM ? kLogitsChunk : kL
 // tokens.  The product still covers 128 rows -- those past AR read whatever
 // follows in shared memory, and no one reads their results -- but the stages get
 // smaller, and more of W is on its way, which is what a call of few tokens waits
-// for.  Epilogue warps of rows past 64 then only hand the accumulator back.  In dX:
-// backward of 64 tokens, 2048 x 32768, 90.3 us with 128 rows of D per stage, 86.7 with 64.
+// for.  Epilogue warps of rows past 64 then only hand the accumulator back.  In dX: backward
+// of 64 tokens, 2048 x 32768, 3.6 us less with 64 rows of D per stage than with 128.
 template <int KIND, int CG, int AR>
 struct HeadTraits {
   static_assert(AR == kHBM || (CG == 1 && KIND <= kHeadDX));

@@ -463,7 +463,8 @@ def linear_distillation(X, W, teacher_logits, teacher_ids, temperature: float = 
 
 
 class LMHead(torch.nn.Module):
-    """The head's weight [V, d] (bf16, N(0, 1/d)) with its two losses."""
+    """The head's weight [V, d] (bf16, N(0, 1/d)) with its two losses.  Nothing here waits for the GPU: a
+    training loop asks device_status() where it reads its loss."""
 
     def __init__(self, d: int, V: int, device=0):
         super().__init__()
