@@ -75,6 +75,11 @@ def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     return t.clone() if t.data_ptr() % 16 else t
 
 
+def _strided(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """t as the library takes what it reads element by element: contiguous."""
+    return None if t is None else t.contiguous()
+
+
 def _elsewhere(index: int, stream: Optional[torch.cuda.Stream], *inputs: Optional[torch.Tensor]):
     """The context a call has to run in when that is not the current one: the given stream, or the
     tensors' GPU.  Outputs and workspace are then allocated there too, and the memory of the inputs is not
@@ -402,7 +407,7 @@ def distill_backward(dloss, X, W, teacher_logits, teacher_ids, lse, temperature:
 class _CrossEntropyFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, labels):
-        X, labels = _dense(X), labels.contiguous()
+        X, labels = _dense(X), _strided(labels)
         loss, lse = cross_entropy_forward(X, W, labels)
         ctx.save_for_backward(X, W, labels, lse)
         return loss
@@ -419,7 +424,7 @@ class _CrossEntropyFunction(torch.autograd.Function):
 class _DistillFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, W, teacher_logits, teacher_ids, temperature):
-        X, teacher_logits, teacher_ids = _dense(X), teacher_logits.contiguous(), teacher_ids.contiguous()
+        X, teacher_logits, teacher_ids = _dense(X), _strided(teacher_logits), _strided(teacher_ids)
         loss, lse = distill_forward(X, W, teacher_logits, teacher_ids, temperature)
         ctx.temperature = temperature
         ctx.save_for_backward(X, W, teacher_logits, teacher_ids, lse)
@@ -436,30 +441,30 @@ class _DistillFunction(torch.autograd.Function):
 
 def _rows(X, **targets):
     """X [..., d] and what each of its rows is trained on, as matrices of that many rows."""
+    if X is None or X.dim() == 2:                    # as they are
+        return [X, *targets.values()]
     lead = X.shape[:-1]
     for name, t in targets.items():
-        if t.shape[:len(lead)] != lead:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected one that starts with {tuple(lead)}")
+        if t is None or t.shape[:len(lead)] != lead:
+            raise ValueError(f"{name}: expected a shape that starts with {tuple(lead)}")
     n = lead.numel()
     return [t.reshape(n, *t.shape[len(lead):]) for t in (X, *targets.values())]
 
 
 def linear_cross_entropy(X, W, labels) -> torch.Tensor:
     """Differentiable per-token loss fp32 [...] of the head W [V, d] on X [..., d] with labels [...]."""
-    if X.dim() == 2:
-        return _CrossEntropyFunction.apply(X, W, labels)
     rows, labels = _rows(X, labels=labels)
-    return _CrossEntropyFunction.apply(rows, W, labels).view(X.shape[:-1])
+    loss = _CrossEntropyFunction.apply(rows, W, labels)
+    return loss if rows is X else loss.view(X.shape[:-1])
 
 
 def linear_distillation(X, W, teacher_logits, teacher_ids, temperature: float = 1.0) -> torch.Tensor:
     """Differentiable per-token distillation loss fp32 [...] of X [..., d] from teacher logits and ids
     [..., K] (the teacher gets no gradient)."""
-    teacher_logits = teacher_logits.detach()
-    if X.dim() == 2:
-        return _DistillFunction.apply(X, W, teacher_logits, teacher_ids, temperature)
     rows, teacher_logits, teacher_ids = _rows(X, teacher_logits=teacher_logits, teacher_ids=teacher_ids)
-    return _DistillFunction.apply(rows, W, teacher_logits, teacher_ids, temperature).view(X.shape[:-1])
+    teacher_logits = None if teacher_logits is None else teacher_logits.detach()
+    loss = _DistillFunction.apply(rows, W, teacher_logits, teacher_ids, temperature)
+    return loss if rows is X else loss.view(X.shape[:-1])
 
 
 class LMHead(torch.nn.Module):
