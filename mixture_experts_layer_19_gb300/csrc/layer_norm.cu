@@ -16,6 +16,7 @@
 //                        sums of dw and db in registers over all its rows and
 //                        prefetches later rows into its own shared memory
 //   rows past 8192 elements are read again instead of kept
+//   fp32 rows whose mean is far from zero beside their spread: rare, read again
 // The backward's per-block column sums go to workspace once per block and are
 // added in a fixed order by a second kernel: no atomics, bitwise repeatable.
 // Measured, bf16 with fp32 weights: forward 16384 x 7168 80 us (5.9 TB/s),
