@@ -128,8 +128,7 @@ def prepare(case, seed):
         if case["prec"] != BF16:
             # the values that the weights' blocks stand for, quantised once, for the plain form
             both = torch.maximum(s["Wg"].abs().max(), s["Wu"].abs().max()).float()
-            top = torch.stack((both, both, s["Wd"].abs().max().float()))
-            s["g"] = top / torch.full_like(top, 2688.0)          # by a number torch multiplies with its reciprocal
+            s["g"] = torch.stack((both, both, s["Wd"].abs().max().float())) / 2688.0
             for i, name in enumerate(("Wg", "Wu", "Wd")):
                 V = s["V" + name[1]] = torch.empty_like(s[name])
                 for e in range(E):
