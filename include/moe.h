@@ -185,6 +185,16 @@ moe_status_t moe_backward(moe_plan_t plan, int64_t T, const void* dY, const void
 moe_status_t moe_quantize_weights(moe_plan_t plan, const void* Wg, const void* Wu, const void* Wd,
                                   moe_stream_t stream);
 
+/* NVFP4 plans: the same with tensor scales that the caller has (a checkpoint's, or a
+ * calibration's) instead of fl32(amax / 2688): scales = 2 device floats, [0] Wg and Wu
+ * together, [1] Wd, as moe_nv_weight_scales gives them; positive and finite (not checked).
+ * Which side of a border between two codes a weight falls on can hang on a scale's last
+ * place, so weights that are to match another program's codes need its scales.  A block
+ * whose largest value is above 2688 times the scale saturates.  Errors as for
+ * moe_quantize_weights, and MOE_ERR_INVALID_ARG for another plan or null or misaligned scales. */
+moe_status_t moe_quantize_weights_scaled(moe_plan_t plan, const void* Wg, const void* Wu, const void* Wd,
+                                         const float* scales, moe_stream_t stream);
+
 /* Quantise a bf16 row-major [rows, K] device matrix to MXFP8 along K
  * (K % 128 == 0): q [rows, K] E4M3 bytes; sf the E8M0 scale bytes
  * (X + 127 with X = floor(log2 amax) - 8 clamped to [-127, 127], all-zero

@@ -1732,7 +1732,9 @@ moe_status_t moe_nv_quantize_transposed(const void* src, int64_t E, int64_t A, i
   return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_nv_quantize_transposed: launch");
 }
 
-moe_status_t moe_quantize_weights(moe_plan_t p, const void* Wg, const void* Wu, const void* Wd, moe_stream_t stream) {
+// scales: the NVFP4 tensor scales [Wg and Wu, Wd] on the device, or null: taken from the weights.
+static moe_status_t quantize_weights(moe_plan_t p, const void* Wg, const void* Wu, const void* Wd, const float* scales,
+                                     moe_stream_t stream) {
   if (!p) return fail(MOE_ERR_INVALID_ARG, "moe_quantize_weights: null plan");
   const moe_config_t& c = p->cfg;
   if (c.prec != MOE_MXFP8 && c.prec != MOE_NVFP4)
@@ -1750,8 +1752,13 @@ moe_status_t moe_quantize_weights(moe_plan_t p, const void* Wg, const void* Wu, 
     const float* g_gu = p->nv_scale;
     const float* g_d = p->nv_scale + 1;
     err = timed_launch(p, "quant_weights", st, [&] {
-      cudaError_t e = launch_nv_tensor_scale(Wg, EF * c.d, Wu, EF * c.d, p->nv_scale, grid, st);
-      if (e == cudaSuccess) e = launch_nv_tensor_scale(Wd, Ed * c.F, nullptr, 0, p->nv_scale + 1, grid, st);
+      cudaError_t e;
+      if (scales) {
+        e = cudaMemcpyAsync(p->nv_scale, scales, 2 * sizeof(float), cudaMemcpyDeviceToDevice, st);
+      } else {
+        e = launch_nv_tensor_scale(Wg, EF * c.d, Wu, EF * c.d, p->nv_scale, grid, st);
+        if (e == cudaSuccess) e = launch_nv_tensor_scale(Wd, Ed * c.F, nullptr, 0, p->nv_scale + 1, grid, st);
+      }
       if (e == cudaSuccess) e = launch_nv_quant_rows(Wg, EF, c.d, g_gu, p->Wgq, p->Wgs, grid, st);
       if (e == cudaSuccess) e = launch_nv_quant_rows(Wu, EF, c.d, g_gu, p->Wuq, p->Wus, grid, st);
       if (e == cudaSuccess) e = launch_nv_quant_rows(Wd, Ed, c.F, g_d, p->Wdq, p->Wds, grid, st);
@@ -1775,6 +1782,20 @@ moe_status_t moe_quantize_weights(moe_plan_t p, const void* Wg, const void* Wu, 
   if (err != cudaSuccess) return cuda_fail(err, "moe_quantize_weights: launch");
   p->weights_quantized = true;
   return MOE_OK;
+}
+
+moe_status_t moe_quantize_weights(moe_plan_t p, const void* Wg, const void* Wu, const void* Wd, moe_stream_t stream) {
+  return quantize_weights(p, Wg, Wu, Wd, nullptr, stream);
+}
+
+moe_status_t moe_quantize_weights_scaled(moe_plan_t p, const void* Wg, const void* Wu, const void* Wd,
+                                         const float* scales, moe_stream_t stream) {
+  if (!p) return fail(MOE_ERR_INVALID_ARG, "moe_quantize_weights_scaled: null plan");
+  if (p->cfg.prec != MOE_NVFP4)
+    return fail(MOE_ERR_INVALID_ARG, "moe_quantize_weights_scaled: plan is not MOE_NVFP4");
+  if (!scales || (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return fail(MOE_ERR_INVALID_ARG, "moe_quantize_weights_scaled: null or misaligned scales");
+  return quantize_weights(p, Wg, Wu, Wd, scales, stream);
 }
 
 moe_status_t moe_plan_padded_rows(moe_plan_t p, int64_t* rows) {

@@ -45,7 +45,7 @@ EXPORTED = ("moe_plan", "moe_plan_destroy", "moe_saved_bytes", "moe_forward", "m
             "moe_layer_norm_forward", "moe_layer_norm_workspace_bytes", "moe_layer_norm_backward",
             "moe_head_workspace_bytes", "moe_head_info", "moe_cross_entropy_forward", "moe_cross_entropy_backward",
             "moe_distill_forward", "moe_distill_backward", "moe_forward_few", "moe_process_logits",
-            "moe_linear_workspace_bytes", "moe_linear")
+            "moe_linear_workspace_bytes", "moe_linear", "moe_quantize_weights_scaled")
 
 
 class moe_config_t(ctypes.Structure):
@@ -101,6 +101,7 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         "moe_last_error": [],
         "moe_route_noalloc": [I64, I32, I32, FP, VP, VP, VP, VP, VP, VP, P],
         "moe_quantize_weights": [P, VP, VP, VP, P],
+        "moe_quantize_weights_scaled": [P, VP, VP, VP, FP, P],
         "moe_mx_quantize": [VP, I64, I64, VP, VP, P],
         "moe_mx_quantize_transposed": [VP, I64, I64, I64, VP, VP, P],
         "moe_plan_info": [P, ctypes.POINTER(I32), ctypes.POINTER(I32)],
@@ -459,9 +460,17 @@ class Plan:
                                      _ptr(out["dest"]), _stream(stream)), "moe_get_routing")
         return out
 
-    def quantize_weights(self, Wg, Wu, Wd, stream=None):
-        """MXFP8 / NVFP4 plans: fill the plan's quantised weight copies (once per weight update)."""
+    def quantize_weights(self, Wg, Wu, Wd, stream=None, scales=None):
+        """MXFP8 / NVFP4 plans: fill the plan's quantised weight copies (once per weight update).  NVFP4: with
+        `scales` (fp32 [2] on the GPU, [Wg and Wu, Wd]) in the place of the tensor scales taken from the weights."""
         self._expect_weights(Wg, Wu, Wd)
+        if scales is not None:
+            _expect(scales, "scales", (2,), torch.float32)
+            if scales.device != self.device or not scales.is_contiguous():
+                raise ValueError(f"scales: must be a contiguous tensor on {self.device}")
+            _check(lib().moe_quantize_weights_scaled(self.handle, _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(scales),
+                                                     _stream(stream)), "moe_quantize_weights_scaled")
+            return
         _check(lib().moe_quantize_weights(self.handle, _ptr(Wg), _ptr(Wu), _ptr(Wd), _stream(stream)),
                "moe_quantize_weights")
 
