@@ -124,7 +124,9 @@ typedef struct moe_plan_s* moe_plan_t;
  * orientations for its block-scaled forward and dgrad GEMMs; its weight
  * gradients are block-scaled GEMMs on operands quantised along the tokens;
  * NVFP4 plans run the separate-kernel schedule).  Otherwise
- * MOE_ERR_UNSUPPORTED / MOE_ERR_INVALID_ARG; allocation failure MOE_ERR_OOM. */
+ * MOE_ERR_UNSUPPORTED / MOE_ERR_INVALID_ARG; allocation failure MOE_ERR_OOM.
+ * Returns when the plan's counters are zeroed (which waits for work queued on the
+ * default stream), so that its first call may run on any stream. */
 moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out);
 
 /* Free the plan's workspace (synchronises its device first). NULL is a no-op.

@@ -902,6 +902,9 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     }
     if (err == cudaSuccess) err = prepare_ep();
   }
+  // The counters and the status word were zeroed on the legacy stream, which streams made without blocking do not wait
+  // for: a call on one of them must not find them as cudaMalloc left them.
+  if (err == cudaSuccess) err = cudaStreamSynchronize(cudaStreamLegacy);
   if (err != cudaSuccess) {
     if (p->few_ws) cudaFree(p->few_ws);
     if (p->ep_ws) cudaFree(p->ep_ws);
@@ -911,7 +914,7 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     if (p->ring_ws) cudaFree(p->ring_ws);
     cudaFree(p->ws);
     delete p;
-    return cuda_fail(err, "moe_plan: router workspace / GEMM attribute");
+    return cuda_fail(err, "moe_plan: workspace / kernel attribute");
   }
   *out = p;
   return MOE_OK;
