@@ -495,7 +495,9 @@ class LMHead(torch.nn.Module):
 
     def sampling_logits(self, X, A=None, B=None, adapter_ids=None, scale=None, dtype=_F32, **processing):
         """logits() of X [T, d], processed in place: `processing` is serve.process_logits's history, penalties,
-        biases and masks."""
+        biases and masks.  Both run on the current stream; there is no `stream=`."""
         from . import serve
+        if "stream" in processing:
+            raise ValueError("stream: both calls run on the current stream (torch.cuda.stream)")
         z = self.logits(X, A, B, adapter_ids, scale, dtype)
         return serve.process_logits(z, **processing, out=z)
