@@ -563,7 +563,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 8; i += TR::per) {
               float x0 = __uint_as_float(v0[i]), x1 = __uint_as_float(v1[i]);
-              if constexpr (TR::per == 2) x0 += __uint_as_float(v0[i + 1]), x1 += __uint_as_float(v1[i + 1]);
+              if constexpr (TR::per == 2) {
+                // an infinite h has left inf - inf behind: its own product stands alone
+                x0 = fabsf(x0) < INFINITY ? x0 + __uint_as_float(v0[i + 1]) : x0;
+                x1 = fabsf(x1) < INFINITY ? x1 + __uint_as_float(v1[i + 1]) : x1;
+              }
               if (r < n) take(x0, x1);
             }
           }
