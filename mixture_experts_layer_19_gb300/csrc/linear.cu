@@ -101,6 +101,15 @@ __device__ __forceinline__ int adapter_of(const LinArgs& g, int t) {
 }
 __device__ __forceinline__ int rank_slices(const LinArgs& g) { return (g.r + 31) / 32; }
 
+// v as a bf16 value, and what that leaves.  A finite v beyond the largest bf16 value takes that one; an infinite one
+// leaves nothing (inf - inf would make NaN of its products).
+__device__ __forceinline__ float bf16_part(float v) {
+  constexpr float kMost = 3.38953139e38f;
+  const float b = __bfloat162float(__float2bfloat16_rn(v));
+  return fabsf(v) < INFINITY ? fminf(fmaxf(b, -kMost), kMost) : b;
+}
+__device__ __forceinline__ float bf16_rest(float v, float b) { return fabsf(b) < INFINITY ? v - b : 0.0f; }
+
 // u of one token and rank index: three bf16 values, pc columns apart.  A rank that ends inside a product's 16
 // columns has zeros behind it (they meet zeros of B, but must not be NaN).
 __device__ __forceinline__ __nv_bfloat16* u_at(const LinArgs& g, int t, int j) {
@@ -110,9 +119,9 @@ __device__ __forceinline__ void put_u(const LinArgs& g, int t, int j, float v) {
   __nv_bfloat16* p = u_at(g, t, j);
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-    p[g.pc * i] = b;
-    v -= __bfloat162float(b);
+    const float b = bf16_part(v);
+    p[g.pc * i] = __float2bfloat16_rn(b);
+    v = bf16_rest(v, b);
     if (g.r % 16 && j >= g.r - 8) p[g.pc * i + 8] = __float2bfloat16_rn(0.0f);
   }
 }
@@ -620,10 +629,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) lin_kernel(const __grid_consta
             uint4* p = reinterpret_cast<uint4*>(u_at(g, t0 + lane, j));
 #pragma unroll
             for (int o = 0; o < 3; ++o) {
-              p[g.pc / 8 * o] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+              float b[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) b[i] = bf16_part(x[i]);
+              p[g.pc / 8 * o] = make_uint4(pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3]), pack_bf16(b[4], b[5]), pack_bf16(b[6], b[7]));
               if (g.r % 16 && j == g.r - 8) p[g.pc / 8 * o + 1] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] -= __bfloat162float(__float2bfloat16_rn(x[i]));
+              for (int i = 0; i < 8; ++i) x[i] = bf16_rest(x[i], b[i]);
             }
           }
         }
