@@ -569,7 +569,7 @@ moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* X, const voi
  *   z = z - frequency[t] n - presence[t]                if v occurs n > 0 times in the generated part
  *   z = z + bias[t, i] for every i with bias_ids[t, i] = v (in the order of i)
  *   z = -inf                                            if the row's mask has a 0 at v
- * in fp32, rounded once.  The first lengths[t] of the L history entries are in use (all
+ * one operation at a time in fp32 (IEEE 754), rounded once to the output's type.  The first lengths[t] of the L history entries are in use (all
  * of them if NULL; lengths past L count as L), the first prompt_lengths[t] of which are the
  * prompt (none if NULL), which only `repetition` looks at.  Ids outside [0, V)
  * take part in nothing.  Mask row m has bit v % 32 of word v / 32 for column v;

@@ -4,9 +4,9 @@
 //   z = logits[t, v]
 //   z = z > 0 ? z / repetition_t : z * repetition_t     if v occurs in the row's history
 //   z = z - frequency_t * n - presence_t                if v was generated n > 0 times
-//   z = z + sum of the row's biases with id v
+//   z = z + each of the row's biases with id v, in their order
 //   z = -inf                                            if the row's mask leaves v out
-// in fp32, rounded once to the type of the logits.
+// in fp32, an operation at a time as they stand here, rounded once to the type of the logits.
 //
 // A block owns a range of columns of one row.  Its logits go into registers; while they are on their way the block
 // counts the row's history into one word per column in shared memory (integer atomics: the result does not depend
@@ -14,10 +14,11 @@
 // are, masked, and the others worked out.  Where histories are long, up to eight of a row's blocks make a
 // cluster and count an eighth of it each, into the block that owns the column.
 //
-// What bounds it (in a graph; HBM would take 5.3 us for 64 rows of 65536 in fp32): 6.1 us with histories of 512, 18.6
-// with 8192, half of them in use, where each warp meets a marked column at nearly every step.  Lists of the
-// marked columns, each worked out by a thread of its own, were no faster (20.7), nor were blocks of 512
-// threads, half the columns to a block, or each block counting the whole history (27 with 16384 columns to a block).
+// What bounds it (in a graph; HBM would take 5.3 us for 64 rows of 65536 in fp32): 6.6 us with histories of 512, 20.3
+// with 8192, half of them in use, where each warp meets a marked column at nearly every step.  Of these 1.2 are the
+// division (a product with the reciprocal, which rounds twice and overflows where z / repetition does not: 19.1).  Tried
+// with the reciprocal, against 18.6: lists of the marked columns, each worked out by a thread of its own (20.7), blocks of
+// 512 threads, half the columns to a block, and each block counting the whole history (27 with 16384 columns to a block).
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -37,12 +38,12 @@ using namespace moe;
 constexpr int kThreads = 256;
 constexpr int kMaxBias = 1024;
 // Histories up to this length are read by every block of a row on its own: a cluster's two
-// barriers cost more (300 rows of 50001 in bf16, histories of 777: 30.0 us against 24.2; one row of 131072 with 8192: 5.6
+// barriers cost more (300 rows of 50001 in bf16, histories of 777: 32.2 us against 25.9; one row of 131072 with 8192: 5.8
 // us in clusters, 8.0 alone).
 constexpr int64_t kAlone = 2048;
 constexpr int64_t kMaxHistory = (1 << 20) - 1;
-// A column's word: how often it was generated, whether the history holds it, the bias entry that
-// carries its sum (plus one).
+// A column's word: how often it was generated, whether the history holds it, its first bias
+// entry (plus one).
 constexpr uint32_t kCountMask = (1u << 20) - 1, kSeen = 1u << 20;
 constexpr int kBiasShift = 21;
 
@@ -98,14 +99,16 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // X: type of the logits; NV: 16-byte vectors per thread; a block's columns: kThreads * NV vectors.
+// (The most vectors, 8192 columns, took 76 registers with the division: three blocks to an SM, 28.4 us where four take 20.3.)
 template <class X, int NV>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant__ LogitsArgs g) {
+__global__ void __launch_bounds__(kThreads, NV * Vec<X>::n == 32 ? 4 : 1) logits_kernel(const __grid_constant__ LogitsArgs g) {
   constexpr int W = Vec<X>::n, kPer = W / 4;
   constexpr int kCols = kThreads * NV * W;
-  extern __shared__ __align__(16) uint32_t word[];   // [kCols], then the biases' columns and sums, [K] each
+  extern __shared__ __align__(16) uint32_t word[];   // [kCols], then the biases' columns, values and successors, [K] each
   const moe_logits_t& a = g.a;
   int* bias_col = reinterpret_cast<int*>(word + kCols);
-  float* bias_sum = reinterpret_cast<float*>(bias_col + a.K);
+  float* bias_val = reinterpret_cast<float*>(bias_col + a.K);
+  int* bias_next = reinterpret_cast<int*>(bias_val + a.K);       // the next entry with the same id, or -1
   const int tid = threadIdx.x;
   const uint32_t row_ = blockIdx.x / g.chunks, chunk = blockIdx.x - row_ * g.chunks;
   const uint32_t rank = chunk % g.cluster;            // of the block in its cluster
@@ -143,6 +146,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
     for (int i = tid; i < a.K; i += kThreads) {
       const int64_t v = load_id(a.bias_ids, row * a.ld_bias_ids + i, a.bias_ids_int64);
       bias_col[i] = v >= 0 && v < a.V && v - c0 >= 0 && v - c0 < kCols ? (int)(v - c0) : -1;
+      bias_val[i] = __ldg(a.bias + row * a.ld_bias + i);
     }
     if (counts) {
       const int len = (int)min(max(said, (int64_t)0), a.L);
@@ -175,34 +179,27 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
     } else {
       __syncthreads();
     }
-    // One of the entries with one id takes their sum, in the entries' order.
+    // The first entry with an id stands in its column's word, the others follow it in their order.
     if (a.K > 0) {
       for (int i = tid; i < a.K; i += kThreads) {
         const int c = bias_col[i];
         if (c < 0) continue;
-        uint32_t w = word[c], old;
-        do {
-          old = w;
-          if (old >> kBiasShift) break;               // another one has it
-          w = atomicCAS(word + c, old, old | (uint32_t)(i + 1) << kBiasShift);
-        } while (w != old);
-        if (old >> kBiasShift) continue;
-        float s = 0.0f;
-        for (int j = 0; j < a.K; ++j)
-          if (bias_col[j] == c) s += __ldg(a.bias + row * a.ld_bias + j);
-        bias_sum[i] = s;
+        bool first = true;
+        for (int j = 0; j < i && first; ++j) first = bias_col[j] != c;
+        int next = i + 1;
+        while (next < a.K && bias_col[next] != c) ++next;
+        bias_next[i] = next < a.K ? next : -1;
+        if (first) word[c] |= (uint32_t)(i + 1) << kBiasShift;     // no other thread writes here
       }
       __syncthreads();
     }
   }
 
-  // a division is a product with the reciprocal (one rounding more), the same for every column
-  const float inv = 1.0f / rep;
   auto finish = [&](float z, uint32_t w) {
-    const uint32_t n = w & kCountMask, b = w >> kBiasShift;
-    z *= (w & (kSeen | kCountMask)) == 0 ? 1.0f : z > 0.0f ? inv : rep;
-    if (n) z -= fmaf(freq, (float)n, pres);
-    if (b) z += bias_sum[b - 1];
+    const uint32_t n = w & kCountMask;
+    if (w & (kSeen | kCountMask)) z = z > 0.0f ? __fdiv_rn(z, rep) : z * rep;
+    if (n) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)n)), pres);
+    for (int i = (int)(w >> kBiasShift) - 1; i >= 0; i = bias_next[i]) z += bias_val[i];
     return z;
   };
   const bool copies = static_cast<const void*>(src) != static_cast<const void*>(dst);
@@ -224,15 +221,21 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
           u[0] = u[kPer - 1];
           u[kPer - 1] = other;
         }
-        uint32_t any = 0;
+        // The marked elements one by one: a warp takes as many steps as its fullest lane has of them, not one per element.
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+        uint32_t left = 0;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) any |= u[e].x | u[e].y | u[e].z | u[e].w;
-        if (any) {
-          write = true;
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+        for (int e = 0; e < W; ++e) left |= w[e] ? 1u << e : 0u;
+        write |= left != 0;
+#pragma unroll 1
+        for (; left; left &= left - 1) {
+          const int e = __ffs(left) - 1;
+          uint32_t v = x[0];
 #pragma unroll
-          for (int e = 0; e < W; ++e)
-            if (w[e]) Vec<X>::put(x[e / kPer], e % kPer, finish(Vec<X>::get(x[e / kPer], e % kPer), w[e]));
+          for (int o = 1; o < 4; ++o) v = e / kPer == o ? x[o] : v;
+          Vec<X>::put(v, e % kPer, finish(Vec<X>::get(v, e % kPer), word[at + e]));
+#pragma unroll
+          for (int o = 0; o < 4; ++o) x[o] = e / kPer == o ? v : x[o];
         }
       }
       if (mask) {
@@ -272,8 +275,8 @@ template <class X, int NV>
 cudaError_t launch(const LogitsArgs& g, cudaStream_t st) {
   constexpr int64_t cols = kThreads * NV * Vec<X>::n;
   const bool counts = g.a.history && (g.a.repetition || g.a.frequency || g.a.presence);
-  const size_t smem = counts || g.a.K > 0 ? cols * 4 + g.a.K * 8 : 0;
-  static_assert(cols * 4 + kMaxBias * 8 <= 48 * 1024, "shared memory");
+  const size_t smem = counts || g.a.K > 0 ? cols * 4 + g.a.K * 12 : 0;
+  static_assert(cols * 4 + kMaxBias * 12 <= 48 * 1024, "shared memory");
   if (smem > 16 * 1024) {   // six blocks to an SM
     const cudaError_t e = cudaFuncSetAttribute(logits_kernel<X, NV>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                                cudaSharedmemCarveoutMaxShared);
