@@ -126,7 +126,10 @@ typedef struct moe_plan_s* moe_plan_t;
  * NVFP4 plans run the separate-kernel schedule).  Otherwise
  * MOE_ERR_UNSUPPORTED / MOE_ERR_INVALID_ARG; allocation failure MOE_ERR_OOM.
  * Returns when the plan's counters are zeroed (which waits for work queued on the
- * default stream), so that its first call may run on any stream. */
+ * default stream), so that its first call may run on any stream.
+ * Beside what grows with T_max, a plan holds moe_forward_few's workspace: for each of
+ * t = min(T_max, 64) tokens 4 KB per SM, 4 k d bytes of results and 4 k F of h in bf16 (k F, or k F / 2,
+ * block-scaled), 59 MB for t = 64 at d 7168, F 2048, top 8.  MOE_DEBUG_IDENTITY_EXPERTS: none. */
 moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out);
 
 /* Free the plan's workspace (synchronises its device first). NULL is a no-op.

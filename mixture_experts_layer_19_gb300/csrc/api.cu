@@ -301,7 +301,7 @@ cudaError_t few_workspace(moe_plan_s* p) {
   };
   const size_t o_h = take(h_rows * h_row), o_hs = take(q ? active * groups_F * 512 : 0);
   const size_t o_xq = take(q ? T * (nv ? c.d / 2 : c.d) : 0), o_xs = take(q ? groups_d * 512 : 0);
-  const size_t o_y = take(pairs * c.d * 4), o_part = take((size_t)4 * p->num_sms * kFewTokens * 256 * 4);
+  const size_t o_y = take(pairs * c.d * 4), o_part = take((size_t)4 * p->num_sms * T * 256 * 4);
   const size_t o_l = take(T * c.E * 4), o_c = take(p->few_ctr_bytes);
   cudaError_t err = cudaMalloc(&p->few_ws, o);
   if (err != cudaSuccess) return err;
@@ -886,7 +886,7 @@ moe_status_t moe_plan(const moe_config_t* cfg, moe_plan_t* out) {
     err = cudaMalloc(&p->router_part, (size_t)std::max(fwd, dw) * sizeof(float));
   }
   if (err == cudaSuccess) err = prepare_gemm_router();
-  if (err == cudaSuccess) err = few_workspace(p);
+  if (err == cudaSuccess && !(c.debug_flags & MOE_DEBUG_IDENTITY_EXPERTS)) err = few_workspace(p);
   if (err == cudaSuccess && c.ep_ranks >= 2) {
     const size_t pairs = (size_t)c.T_max * c.k;
     // <u, h> partials per pair: F/256 (bf16 u GEMM) or F/128 (block-scaled)
@@ -1534,6 +1534,7 @@ moe_status_t moe_forward_few(moe_plan_t p, int64_t T, const void* X, const float
   a.F = c.F;
   a.E = c.E;
   a.k = c.k;
+  a.part_rows = (int)std::min<int64_t>(c.T_max, kFewTokens);
   a.stall = (c.debug_flags & MOE_DEBUG_STALL_TEST) != 0;
   const size_t smem = moe_few_smem(c.prec, a.T, c.E, c.k, &a.stages, &a.b_bytes);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const __grid_co
         // Where CTA c puts its part of a tile: a range has two cut tiles at most in each phase, one that began
         // before it (`inside`) and one that it leaves unfinished.
         auto part_slot = [&](int c, bool inside) {
-          return (size_t)((2 * c + (inside ? 0 : 1)) * 2 + phase) * kFewTokens * kFewRows + r0;
+          return (size_t)((2 * c + (inside ? 0 : 1)) * 2 + phase) * g.part_rows * kFewRows + r0;
         };
         // One sorted row's two values, finished: h of a column of F, or y of two columns of d.
         auto finish = [&](int r, float v0, float v1) {

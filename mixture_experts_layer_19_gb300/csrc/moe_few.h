@@ -22,7 +22,7 @@ struct FewArgs {
   const float* ts;                // NVFP4: tensor scales [Wg and Wu, Wd]
   uint8_t* H;                     // [2 T k, F] bf16 (h and what its rounding left), or [T k, F] quantised
   float* y;                       // [T k, d] the experts' results
-  float* part;                    // [4 CTAs][64][256] parts of sums cut between CTAs
+  float* part;                    // [4 CTAs][part_rows][256] parts of sums cut between CTAs
   int *cnt_up, *cnt_dn;           // arrivals of parts, per tile and epilogue warp; zero between launches, as are
   int* ready;                     //   finished parts of h per expert,
   int* done;                      //   epilogue warps that are done,
@@ -31,6 +31,7 @@ struct FewArgs {
   int32_t* status;
   uint64_t timeout_ns;
   int T, d, F, E, k;
+  int part_rows;                  // most tokens that the plan's calls have, 64 at most
   int stages, b_bytes;            // ring stages, bytes of activations per stage
   int n_up, n_dn;                 // how many tile counters there are
   int stall;                      // test hook: no weights are loaded, every wait expires
