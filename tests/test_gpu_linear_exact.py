@@ -1,12 +1,12 @@
 """GPU tests of fp32 results of the projection in norm (tests/linear_norm.py has the bound, and tests/test_linear_norm.py
-what it tells apart)."""
+what it tells apart), and of weights that really pass 2^32 bytes."""
 import numpy as np
 import pytest
 import torch
 
 from mixture_experts_layer_19_gb300.workload import to_f64
 from tests import linear_norm
-from tests.test_gpu_linear import CASES, inputs, on
+from tests.test_gpu_linear import CASES, check, inputs, on
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -47,3 +47,27 @@ def test_adapters_that_outweigh_w_in_norm(serve, T, d, N, n, r):
     s["W"] = (s["W"].float() * 2.0 ** -12).to(torch.bfloat16)
     got = serve.linear(**on(s), out_dtype=torch.float32)
     assert linear_norm.off(to_f64(got), exact(s)) <= linear_norm.tolerance(r)
+
+
+@pytest.mark.parametrize("T,out", [(40, torch.float32), (200, torch.bfloat16), (130, torch.float32)])
+def test_weights_past_32_bits(serve, T, out):
+    """W of 2^33 bytes and more, for up to 64 tokens, on pairs of CTAs and on single ones; the rows at its two ends and where
+    it passes 2^32 bytes are not zero."""
+    d, n, r, N = 512, 2, 8, (1 << 23) + 300
+    g = torch.Generator(device=DEV).manual_seed(T)
+    W = torch.zeros((N, d), dtype=torch.bfloat16, device=DEV)
+    B = torch.zeros((n, N, r), dtype=torch.bfloat16, device=DEV)
+    middle = (1 << 32) // (2 * d)
+    parts = [slice(0, 300), slice(middle - 150, middle + 150), slice(N - 300, N)]
+    for p in parts:
+        W[p] = (torch.randn((300, d), generator=g, device=DEV) / d ** 0.5).to(torch.bfloat16)
+        B[:, p] = torch.randn((n, 300, r), generator=g, device=DEV).to(torch.bfloat16)
+    A = (torch.randn((n, r, d), generator=g, device=DEV) / d ** 0.5).to(torch.bfloat16)
+    X = torch.randn((T, d), generator=g, device=DEV).to(torch.bfloat16)
+    ids = torch.arange(T, device=DEV) % (n + 1)
+    got = serve.linear(X, W, A, B, ids, out_dtype=out)
+    for p in parts:
+        s = {"X": X, "W": W[p], "A": A, "B": B[:, p], "adapter_ids": ids}
+        check(got[:, p].cpu(), {k: v.cpu() for k, v in s.items()})
+    for a, b in zip(parts, parts[1:]):
+        assert not bool(got[:, a.stop:b.start].any())
