@@ -294,7 +294,7 @@ moe_status_t moe_nv_weight_scales(moe_plan_t plan, float* out, moe_stream_t stre
 
 /* The whole layer for up to 64 tokens in one launch: a decode step, which has
  * no backward.  Same formulas, routing rules and block-scaled quantisation of X
- * and h as moe_forward; sums and the experts' results y stay in fp32 until Y is
+ * and h as moe_forward, silu by the fast exponential like it; sums and the experts' results y stay in fp32 until Y is
  * rounded (moe_forward rounds h, and each y, to bf16 first), so the two agree within
  * rounding, not to the bit.
  *   X [T, d] bf16;  logits [T, E] fp32, or NULL with the router's weight
@@ -572,9 +572,10 @@ moe_status_t moe_linear(const moe_linear_config_t* cfg, const void* X, const voi
  *   z = z - frequency[t] n - presence[t]                if v occurs n > 0 times in the generated part
  *   z = z + bias[t, i] for every i with bias_ids[t, i] = v (in the order of i)
  *   z = -inf                                            if the row's mask has a 0 at v
- * one operation at a time in fp32 (IEEE 754), rounded once to the output's type.  The first lengths[t] of the L history entries are in use (all
- * of them if NULL; lengths past L count as L), the first prompt_lengths[t] of which are the
- * prompt (none if NULL), which only `repetition` looks at.  Ids outside [0, V)
+ * one operation at a time in fp32 (IEEE 754), rounded once to the output's type.  The first
+ * lengths[t] of the L history entries are in use (all of them if NULL; lengths past L count as
+ * L), the first prompt_lengths[t] of which are the prompt (none if NULL), which only
+ * `repetition` looks at.  Ids outside [0, V)
  * take part in nothing.  Mask row m has bit v % 32 of word v / 32 for column v;
  * mask_rows[t] is the row of t (t itself if NULL); outside [0, G): no mask.  A
  * row whose mask leaves nothing is all -inf.  What a masked column held, NaN among it, is gone.

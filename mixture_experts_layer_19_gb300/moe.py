@@ -462,7 +462,8 @@ class Plan:
 
     def quantize_weights(self, Wg, Wu, Wd, stream=None, scales=None):
         """MXFP8 / NVFP4 plans: fill the plan's quantised weight copies (once per weight update).  NVFP4: with
-        `scales` (fp32 [2] on the GPU, [Wg and Wu, Wd]) in the place of the tensor scales taken from the weights."""
+        `scales` (fp32 [2] on the GPU, [Wg and Wu, Wd]) in the place of the tensor scales taken from the weights
+        (which is what MoELayer does with its own)."""
         self._expect_weights(Wg, Wu, Wd)
         if scales is not None:
             _expect(scales, "scales", (2,), torch.float32)

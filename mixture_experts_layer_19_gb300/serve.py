@@ -68,7 +68,11 @@ def linear(X, W, A=None, B=None, adapter_ids=None, scale=None, out_dtype=_BF16, 
     X bf16 [T, d], W bf16 [N, d], d a multiple of 8; A bf16 [n, r, d], B bf16 [n, N, r], r a multiple of 8
     up to 256; adapter_ids int32 or int64 [T]; scale fp32 [n] (1 by default); without A, W alone.
     Returns [T, N] of out_dtype (bf16 or fp32), `out` where given.  A wait that expires on the GPU is
-    reported by train.device_status()."""
+    reported by train.device_status().
+
+    Made for adapters and for fp32 results; for bf16 ones without adapters X @ W.T is often as fast or
+    faster (64 x 2048 x 32768: 26 us against 31 here; 4096 x 7168 x 2048: 68 against 78; slower where rows of
+    the result start off 16 bytes, 777 x 1000 x 5001: 72 against 21)."""
     for name, t in (("X", X), ("W", W)):
         if t is None or t.dtype is not _BF16 or t.dim() != 2:
             raise ValueError(f"{name}: expected a 2-d torch.bfloat16 tensor")

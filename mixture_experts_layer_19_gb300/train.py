@@ -487,7 +487,8 @@ class LMHead(torch.nn.Module):
     @torch.no_grad()
     def logits(self, X, A=None, B=None, adapter_ids=None, scale=None, dtype=_F32):
         """The logits [..., V] of X [..., d], with the tokens' low-rank adapters where given (serve.linear's
-        arguments); adapter_ids [...].  No gradient: training uses the losses."""
+        arguments); adapter_ids [...].  No gradient: training uses the losses.  bf16 logits without adapters
+        are a plain product, which torch's may do faster: serve.linear has figures."""
         from . import serve
         rows, ids = _rows(X, adapter_ids=adapter_ids) if A is not None else (_rows(X)[0], adapter_ids)
         z = serve.linear(_dense(rows), self.weight, A, B, _strided(ids), scale, out_dtype=dtype)
